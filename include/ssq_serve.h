@@ -1,0 +1,160 @@
+/*
+ * ssq_serve.h -- libssq: what a serving engine does with the state pool of
+ * ssq.h around the decode step.
+ *
+ *   ssq_prefill_ragged   prompts, pieces of prompts and single tokens of a
+ *                        batch, packed without padding, in one call: the
+ *                        recurrence of ssq.h as linear attention with one
+ *                        decay per head, in chunks (matrix products) or token
+ *                        by token, from the pool's states and back into them.
+ *   ssq_beam_select      the best continuations over a request's beams and
+ *                        the vocabulary.
+ *   ssq_pool_reorder     each beam's slot takes its parent's state
+ *   ssq_damp_pool_reorder  (the same for DAMP pools).
+ *
+ * The conventions of ssq.h hold for every entry point: the caller owns all
+ * memory, argument errors are found on the host before anything is launched,
+ * what can only be seen on the device sets a bit of the pool's error word and
+ * skips the request concerned, launches are asynchronous on `stream`, results
+ * are deterministic, and calls that write the same slot and layer must not
+ * overlap on the GPU.  All pointers belong to the current device.
+ */
+#ifndef SSQ_SERVE_H
+#define SSQ_SERVE_H
+
+#include "ssq.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+/* Further bits of the pool's error word (ssq_pool_error). */
+#define SSQ_DEVERR_TOKENS 0x10u /* a request's token range is not valid       */
+#define SSQ_DEVERR_PARENT 0x20u /* a parent outside [-1, beams), or two beams
+                                   of a request in one slot                   */
+
+#define SSQ_MAX_BEAMS 64 /* beams of a request, and candidates selected */
+
+/* Element types of activations and logits. */
+typedef enum {
+    SSQ_T_BF16 = 0,
+    SSQ_T_F16 = 1,
+    SSQ_T_F32 = 2
+} ssq_dtype;
+
+/* The tokens of a ragged batch, request after request without padding.
+ * A stride is the number of elements from one token to the next (at least
+ * the size of one token's entry), so that x, B and C may be slices of one
+ * fused activation; inside a token the entries are contiguous.
+ *   x, y  [total][nheads][headdim] of `type`
+ *   B, C  [total][ngroups][d_state] of `type`
+ *   dt    [total][nheads] fp32, already positive (softplus and bias applied)
+ * Pointers aligned to their element.  y must not overlap an input. */
+typedef struct {
+    ssq_dtype type;
+    const void* x;
+    const void* B;
+    const void* C;
+    const float* dt;
+    void* y;
+    long long x_stride, B_stride, C_stride, dt_stride, y_stride;
+    long long total;
+} ssq_tokens;
+
+/* Bytes of device workspace that ssq_prefill_ragged takes for a batch of
+ * this size whose longest run has max_len tokens (0: none needed).  Host
+ * only; no CUDA call. */
+SSQ_API ssq_status ssq_prefill_ragged_workspace(const ssq_config* cfg, int batch, int max_len,
+                                                size_t* bytes);
+
+/* Prompts, pieces of prompts and single tokens of one layer.  Request b owns
+ * the tokens cu_tokens[b] .. cu_tokens[b+1]-1 of `tok`; its state S (per head
+ * headdim x d_state) starts from its slot, or from zero where fresh[b] is not
+ * 0, and for each of its tokens in turn
+ *     a = dt_h * A_h                              (fp32 product)
+ *     S = exp(a) S + dt_h x_h B_g^T               (fp32 state)
+ *     y_h = S C_g + D_h x_h                       (rounded once to `type`)
+ * with g = h / (nheads/ngroups); y reads the unrounded state, and after the
+ * last token the state is refit, rounded and written to the slot as
+ * ssq_prefill does.  A request without tokens leaves its slot as it is,
+ * unless it is fresh (then the zero state is written).
+ *
+ * Runs of at least 32 tokens in bf16 (headdim a multiple of 8, d_state at most 128,
+ * strides and pointers of x, B, C multiples of 16 bytes) go through chunks of
+ * 128 tokens on the tensor cores: within a chunk, with cs the running sum of
+ * a,
+ *     y_i = sum_{j<=i} (C_i.B_j) exp(cs_i-cs_j) dt_j x_j + exp(cs_i) S C_i
+ *     S   = exp(cs_L) S + sum_j exp(cs_L-cs_j) dt_j x_j B_j^T
+ * with fp32 sums and state; the products' operands are bf16, the last one's
+ * input taken as a sum of two bf16 parts.  Other runs go token by token in
+ * fp32 arithmetic.  Either way a non-finite x, B, C or dt acts on its own and
+ * later tokens of its own request only; in a chunk a non-finite x_p makes y
+ * and the state of its row p NaN.
+ *
+ *   slot_idx   device int32 [batch] or NULL (slot b)
+ *   cu_tokens  device int32 [batch+1], not decreasing, within [0, total]; a
+ *              request whose range is not valid or is longer than max_len is
+ *              skipped (SSQ_DEVERR_TOKENS)
+ *   max_len    the longest run (or an upper bound)
+ *   fresh      device uint8 [batch] or NULL (none is)
+ *   A, D       device fp32 [nheads]
+ *   workspace  device, 256-byte aligned, at least the bytes of
+ *              ssq_prefill_ragged_workspace; its contents are not kept, so
+ *              calls that may overlap on the GPU need one each.
+ * The y of a skipped request, and of tokens outside every request, is not
+ * written. */
+SSQ_API ssq_status ssq_prefill_ragged(const ssq_config* cfg, void* pool,
+                                      const int32_t* slot_idx, int batch, int layer,
+                                      const int32_t* cu_tokens, int max_len,
+                                      const uint8_t* fresh, const ssq_tokens* tok,
+                                      const float* A, const float* D, void* workspace,
+                                      size_t workspace_bytes, cudaStream_t stream);
+
+/* Beam search's selection.  For request r, beam k with accumulated score
+ * s_k and logits l_k over the vocabulary, candidate (k, t) has the value
+ *     s_k + l_k[t] - logsumexp(l_k)
+ * and the nsel largest of the request's candidates are written in falling
+ * order, of equal ones the lowest k*vocab + t first.  A beam with done != 0
+ * has the one candidate (k, done_token) with the value s_k; its logits are not
+ * read.  A logit of -inf or NaN is no candidate and adds nothing to the sum;
+ * a score that is -inf or NaN, or a logit of +inf, leaves its beam without
+ * candidates.  Places past the last candidate get score -inf, parent -1 and
+ * token -1.
+ *   logits  device [batch][beams][vocab] of `type`, rows logits_stride
+ *           elements apart (requests beams*logits_stride), aligned to the
+ *           element
+ *   scores  device fp32 [batch][beams]
+ *   done    device uint8 [batch][beams] or NULL; done_token in [0, vocab)
+ *   out_score fp32, out_parent int32, out_token int32, device [batch][nsel],
+ *           which may not overlap the inputs
+ * beams and nsel 1 .. SSQ_MAX_BEAMS, beams*vocab below 2^31. */
+SSQ_API ssq_status ssq_beam_select(int batch, int beams, int vocab, ssq_dtype type,
+                                   const void* logits, long long logits_stride,
+                                   const float* scores, const uint8_t* done, int done_token,
+                                   int nsel, float* out_score, int32_t* out_parent,
+                                   int32_t* out_token, cudaStream_t stream);
+
+/* Reordering of the beams' states, in place: for layers layer0 ..
+ * layer0+nl-1, the slot of beam k of request r takes the state that the slot
+ * of its beam parent[r][k] held before the call (bit for bit, every region);
+ * a parent of -1 leaves the slot as it is.
+ *   slot_idx  device int32 [batch][beams] or NULL (slot r*beams + k); the
+ *             slots of one call are distinct
+ *   parent    device int32 [batch][beams], as ssq_beam_select writes it
+ * A request with a slot outside the pool (SSQ_DEVERR_SLOT), or with a parent
+ * out of range or two beams in one slot (SSQ_DEVERR_PARENT), is skipped as a
+ * whole.  beams 1 .. SSQ_MAX_BEAMS. */
+SSQ_API ssq_status ssq_pool_reorder(const ssq_config* cfg, void* pool, const int32_t* slot_idx,
+                                    int batch, int beams, const int32_t* parent, int layer0,
+                                    int nl, cudaStream_t stream);
+
+/* The same for a DAMP pool. */
+SSQ_API ssq_status ssq_damp_pool_reorder(const ssq_damp_config* cfg, void* pool,
+                                         const int32_t* slot_idx, int batch, int beams,
+                                         const int32_t* parent, int layer0, int nl,
+                                         cudaStream_t stream);
+
+#ifdef __cplusplus
+}
+#endif
+#endif /* SSQ_SERVE_H */

@@ -7,6 +7,7 @@
 #include <cstring>
 
 #include "ssq.h"
+#include "ssq_host.h"
 #include "ssq_params.h"
 
 namespace {
@@ -17,6 +18,11 @@ thread_local char g_detail[256] = "";
 // thread.
 thread_local int g_test_withhold = 0;
 thread_local long long g_test_wait_limit = 0;
+
+}  // namespace
+
+namespace ssq {
+namespace host {
 
 ssq_status fail(ssq_status s, const char* fmt, ...)
 {
@@ -32,6 +38,8 @@ ssq_status cuda_fail(cudaError_t e, const char* what)
     return fail(SSQ_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
 }
 
+namespace {
+
 size_t round_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
 
 bool is_quant(ssq_format f) { return f >= SSQ_I8_SYM && f <= SSQ_I4_ASYM; }
@@ -45,6 +53,8 @@ int bits_of(ssq_format f)
     default: return 32;
     }
 }
+
+}  // namespace
 
 bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
 
@@ -163,11 +173,12 @@ ssq_status need(const void* p, const char* name, size_t align)
     return SSQ_OK;
 }
 
-#define SSQ_TRY(x)                         \
-    do {                                   \
-        ssq_status _s = (x);               \
-        if (_s != SSQ_OK) return _s;       \
-    } while (0)
+}  // namespace host
+}  // namespace ssq
+
+using namespace ssq::host;
+
+namespace {
 
 void fill_tiles(const ssq::PoolView& pv, ssq::CallView* cv, int rows_q, int rows_f)
 {
@@ -508,7 +519,9 @@ namespace {
 
 size_t align_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
 
-ssq_status damp_layout_of(const ssq_damp_config* c, ssq_damp_layout* L)
+}  // namespace
+
+ssq_status ssq::host::damp_layout_of(const ssq_damp_config* c, ssq_damp_layout* L)
 {
     if (!c) return fail(SSQ_ERR_INVALID_ARG, "cfg is NULL");
     if (c->n_layers < 1 || c->n_slots < 1)
@@ -539,6 +552,8 @@ ssq_status damp_layout_of(const ssq_damp_config* c, ssq_damp_layout* L)
     L->bits_per_value = (16.0 * K * P + 8.0 * (N - K) * P + 64.0 * (N - K)) / (double)(N * P);
     return SSQ_OK;
 }
+
+namespace {
 
 ssq_status damp_view(const ssq_damp_config* c, void* pool, const int32_t* chan,
                      ssq::DampView* dv)

@@ -1,0 +1,464 @@
+// ssq_beam.cu -- ssq_beam_select: the best continuations of each request over
+// its beams and the vocabulary.
+//
+//   value(k, t) = score_k + (l_k[t] - lse_k),  lse_k = log sum_t exp(l_k[t])
+//
+// One pass over the logits.  Within a row the order of the values is the
+// order of the logits, so a warp can keep the best nsel of its part of a row
+// while it also accumulates that part's running maximum and sum of
+// exponentials; only the short lists meet once lse is known.  A request is
+// one thread-block cluster: every block takes a slice of the vocabulary of
+// all its rows, its 16 warps split rows and slice, the lists of a row are
+// merged in the block, and block 0 reads the others' lists through
+// distributed shared memory, forms the values and merges across rows.  So one
+// launch does it all, without workspace or atomics, and the result does not
+// depend on timing.
+//
+// A warp's list lies across its lanes in falling order (KP entries per lane).
+// A vector of logits touches it only if its largest exceeds the list's last
+// entry, about nsel*(1 + ln(n/nsel)) times in n random logits.  Sums of
+// exponentials are fp32 per lane (at most some thousand terms), joined in
+// double; values are compared in double, since scores of different beams may
+// be near one another.
+#include <cooperative_groups.h>
+#include <cuda_fp16.h>
+
+#include "ssq_common.cuh"
+#include "ssq_serve_params.h"
+
+namespace ssq {
+
+namespace {
+
+namespace cg = cooperative_groups;
+
+constexpr int kBThreads = 512;
+constexpr int kBWarps = kBThreads / 32;
+constexpr int kMaxTasks = SSQ_MAX_BEAMS;         // lists of a block
+constexpr float kLog2e = 1.4426950408889634f;
+
+// The list's order: larger value first, then lower index.
+template <typename V>
+__device__ __forceinline__ bool better(V a, int ia, V b, int ib)
+{
+    return a > b || (a == b && ia < ib);
+}
+
+// A sorted list of the best n entries across the warp's lanes: entry e in
+// slot e/32 of lane e%32.  (tv, ti): its last entry.
+template <typename V, int KP>
+struct TopList {
+    V v[KP];
+    int i[KP];
+    V tv;
+    int ti, n;
+
+    __device__ __forceinline__ void clear(int n_)
+    {
+        n = n_;
+#pragma unroll
+        for (int k = 0; k < KP; ++k) {
+            v[k] = -INFINITY;
+            i[k] = 0x7fffffff;
+        }
+        tv = -INFINITY;
+        ti = 0x7fffffff;
+    }
+    __device__ __forceinline__ void set_last()
+    {
+        const int at = n - 1;
+        if (KP == 1 || at < 32) {
+            tv = __shfl_sync(0xffffffffu, v[0], at & 31);
+            ti = __shfl_sync(0xffffffffu, i[0], at & 31);
+        } else {
+            tv = __shfl_sync(0xffffffffu, v[KP - 1], at & 31);
+            ti = __shfl_sync(0xffffffffu, i[KP - 1], at & 31);
+        }
+    }
+    // Insert an entry (the same in all lanes) that is better than the last.
+    __device__ __forceinline__ void insert(V nv, int ni)
+    {
+        const int lane = threadIdx.x & 31;
+        V carry_v = nv;
+        int carry_i = ni;
+        bool placed = false;
+#pragma unroll
+        for (int k = 0; k < KP; ++k) {
+            // entries of this slot that stay in front of the new one
+            const unsigned front = __ballot_sync(0xffffffffu, better(v[k], i[k], nv, ni));
+            const int at = placed ? 0 : __popc(front);
+            const V up_v = __shfl_up_sync(0xffffffffu, v[k], 1);
+            const int up_i = __shfl_up_sync(0xffffffffu, i[k], 1);
+            const V out_v = __shfl_sync(0xffffffffu, v[k], 31);
+            const int out_i = __shfl_sync(0xffffffffu, i[k], 31);
+            if (at < 32) {
+                if (lane > at) {
+                    v[k] = up_v;
+                    i[k] = up_i;
+                } else if (lane == at) {
+                    v[k] = carry_v;
+                    i[k] = carry_i;
+                }
+                carry_v = out_v;
+                carry_i = out_i;
+                placed = true;
+            }
+        }
+        set_last();
+    }
+    // Offer one entry per lane, in any order; every lane calls this.
+    __device__ __forceinline__ void offer(V nv, int ni)
+    {
+        unsigned m = __ballot_sync(0xffffffffu, better(nv, ni, tv, ti));
+        while (m) {
+            const int src = __ffs(m) - 1;
+            insert(__shfl_sync(0xffffffffu, nv, src), __shfl_sync(0xffffffffu, ni, src));
+            m &= m - 1;
+            m &= __ballot_sync(0xffffffffu, better(nv, ni, tv, ti));
+        }
+    }
+};
+
+template <int TYPE>
+struct Act;
+template <>
+struct Act<SSQ_T_F32> {
+    static constexpr int VEC = 4, BYTES = 4;
+    __device__ static void unpack(uint4 w, float (&f)[4])
+    {
+        f[0] = __uint_as_float(w.x); f[1] = __uint_as_float(w.y);
+        f[2] = __uint_as_float(w.z); f[3] = __uint_as_float(w.w);
+    }
+    __device__ static float one(const void* p, long long i)
+    {
+        return __ldg(reinterpret_cast<const float*>(p) + i);
+    }
+};
+template <>
+struct Act<SSQ_T_BF16> {
+    static constexpr int VEC = 8, BYTES = 2;
+    __device__ static void unpack(uint4 w, float (&f)[8])
+    {
+        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            f[2 * k] = __uint_as_float(u[k] << 16);
+            f[2 * k + 1] = __uint_as_float(u[k] & 0xffff0000u);
+        }
+    }
+    __device__ static float one(const void* p, long long i)
+    {
+        const unsigned short u = __ldg(reinterpret_cast<const unsigned short*>(p) + i);
+        return __uint_as_float((uint32_t)u << 16);
+    }
+};
+template <>
+struct Act<SSQ_T_F16> {
+    static constexpr int VEC = 8, BYTES = 2;
+    __device__ static void unpack(uint4 w, float (&f)[8])
+    {
+        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const float2 t = __half22float2(*reinterpret_cast<const __half2*>(&u[k]));
+            f[2 * k] = t.x;
+            f[2 * k + 1] = t.y;
+        }
+    }
+    __device__ static float one(const void* p, long long i)
+    {
+        return __half2float(__ldg(reinterpret_cast<const __half*>(p) + i));
+    }
+};
+
+// A lane's running maximum and sum of exponentials relative to it.
+struct Sum {
+    float m, s;
+    __device__ __forceinline__ void clear()
+    {
+        m = -INFINITY;
+        s = 0.0f;
+    }
+    // n values whose largest is mx
+    template <int n>
+    __device__ __forceinline__ void add(const float (&f)[n], float mx)
+    {
+        if (mx > m) {
+            s *= exp2f(__fmul_rn(__fsub_rn(m, mx), kLog2e));   // m = -inf: s is 0
+            m = mx;
+        }
+        const float mm = m == -INFINITY ? 0.0f : m;            // all -inf: exp gives 0
+        const float2 nm2 = make_float2(-mm, -mm), l2 = make_float2(kLog2e, kLog2e);
+        float2 a = make_float2(0.0f, 0.0f);
+#pragma unroll
+        for (int k = 0; k + 1 < n; k += 2) {
+            const float2 d = mul2(add2(make_float2(f[k], f[k + 1]), nm2), l2);
+            a = add2(a, make_float2(exp2f(d.x), exp2f(d.y)));
+        }
+        if constexpr (n % 2 == 1) a.x += exp2f(__fmul_rn(__fsub_rn(f[n - 1], mm), kLog2e));
+        s += a.x + a.y;
+    }
+};
+
+struct BeamShared {
+    float v[kMaxTasks * SSQ_MAX_BEAMS];   // lists of logits, nsel apart
+    int i[kMaxTasks * SSQ_MAX_BEAMS];
+    double sum[kMaxTasks];                // sum of exponentials relative to max
+    float max[kMaxTasks];
+    double lse[SSQ_MAX_BEAMS];
+};
+struct FinalShared {
+    double v[kBWarps * SSQ_MAX_BEAMS];
+    int i[kBWarps * SSQ_MAX_BEAMS];
+};
+
+template <int TYPE, int KP>
+__global__ void __launch_bounds__(kBThreads, 2)
+beam_kernel(const __grid_constant__ BeamCall bc)
+{
+    using T = Act<TYPE>;
+    constexpr int VEC = T::VEC, U = 4;
+    extern __shared__ __align__(16) unsigned char smem_raw[];
+    BeamShared& sh = *reinterpret_cast<BeamShared*>(smem_raw);
+    FinalShared& fin = *reinterpret_cast<FinalShared*>(smem_raw + sizeof(BeamShared));
+
+    cg::cluster_group cluster = cg::this_cluster();
+    const int CS = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
+    const int req = blockIdx.x / CS;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int K = bc.beams, V = bc.vocab, nsel = bc.nsel;
+    const int wpr = K <= kBWarps ? kBWarps / K : 1;       // warps per row
+    const int pieces = CS * wpr;
+    // whole vectors per piece, so that a piece's start keeps the row's alignment
+    const int plen = ((V + pieces - 1) / pieces + VEC - 1) / VEC * VEC;
+
+    for (int task = warp; task < K * wpr; task += kBWarps) {
+        const int row = task / wpr, sub = task - row * wpr;
+        TopList<float, KP> top;
+        top.clear(nsel);
+        Sum sum;
+        sum.clear();
+        const int piece = rank * wpr + sub;
+        if (bc.done && bc.done[(long long)req * K + row]) {
+            if (piece == 0) top.insert(0.0f, bc.done_token);
+        } else {
+            const long long lo = (long long)piece * plen;
+            const int n = (int)max(0LL, min((long long)plen, V - lo));
+            const char* base = reinterpret_cast<const char*>(bc.logits)
+                               + (((long long)req * K + row) * bc.stride + lo) * T::BYTES;
+            // single logits up to the first 16-byte boundary and after the last
+            const int head = min(n, (int)((16 - ((uintptr_t)base & 15)) & 15) / T::BYTES);
+            const int nvec = (n - head) / VEC;
+            const int tail0 = head + nvec * VEC;
+            const int first = (int)lo;
+            auto edge = [&](int from, int to) {   // at most VEC - 1 logits
+                float f[1] = {-INFINITY};
+                if (from + lane < to) f[0] = fmaxf(T::one(base, from + lane), -INFINITY);
+                sum.add(f, f[0]);
+                top.offer(f[0], f[0] == -INFINITY ? 0x7fffffff : first + from + lane);
+            };
+            edge(0, head);
+            const uint4* vp = reinterpret_cast<const uint4*>(base + (long long)head * T::BYTES);
+            for (int v0 = 0; v0 < nvec; v0 += 32 * U) {
+                uint4 w[U];
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    const int at = v0 + u * 32 + lane;
+                    if (at < nvec) w[u] = __ldcs(vp + at);
+                }
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    const int at = v0 + u * 32 + lane;
+                    float f[VEC];
+                    T::unpack(w[u], f);
+                    float mx = -INFINITY;
+#pragma unroll
+                    for (int k = 0; k < VEC; ++k) {
+                        f[k] = at < nvec ? fmaxf(f[k], -INFINITY) : -INFINITY;   // NaN: -inf
+                        mx = fmaxf(mx, f[k]);
+                    }
+                    sum.add(f, mx);
+                    if (__any_sync(0xffffffffu, mx > top.tv)) {
+                        const int i0 = first + head + at * VEC;
+#pragma unroll 1
+                        for (int k = 0; k < VEC; ++k) {
+                            float fk = f[0];
+#pragma unroll
+                            for (int e = 1; e < VEC; ++e) fk = k == e ? f[e] : fk;
+                            top.offer(fk, fk == -INFINITY ? 0x7fffffff : i0 + k);
+                        }
+                    }
+                }
+            }
+            edge(tail0, n);
+        }
+        // the warp's maximum and sum
+        float m = sum.m;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        double s = sum.m == -INFINITY ? 0.0 : (double)sum.s * exp((double)sum.m - (double)m);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+        if (lane == 0) {
+            sh.max[task] = m;
+            sh.sum[task] = s;
+        }
+#pragma unroll
+        for (int k = 0; k < KP; ++k)
+            if (lane + 32 * k < nsel) {
+                sh.v[task * nsel + lane + 32 * k] = top.v[k];
+                sh.i[task * nsel + lane + 32 * k] = top.i[k];
+            }
+    }
+    __syncthreads();
+
+    // merge a row's lists into its first (K <= 16; otherwise there is one)
+    if (wpr > 1 && warp < K) {
+        const int t0 = warp * wpr;
+        TopList<float, KP> top;
+        top.clear(nsel);
+        float m = -INFINITY;
+        for (int t = t0; t < t0 + wpr; ++t) {
+            m = fmaxf(m, sh.max[t]);
+#pragma unroll
+            for (int k = 0; k < KP; ++k) {
+                const int e = lane + 32 * k;
+                const bool has = e < nsel;
+                top.offer(has ? sh.v[t * nsel + e] : -INFINITY,
+                          has ? sh.i[t * nsel + e] : 0x7fffffff);
+            }
+        }
+        double s = 0.0;
+        if (lane < wpr && sh.max[t0 + lane] != -INFINITY)
+            s = sh.sum[t0 + lane] * exp((double)sh.max[t0 + lane] - (double)m);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+        __syncwarp();
+        if (lane == 0) {
+            sh.max[t0] = m;
+            sh.sum[t0] = s;
+        }
+#pragma unroll
+        for (int k = 0; k < KP; ++k)
+            if (lane + 32 * k < nsel) {
+                sh.v[t0 * nsel + lane + 32 * k] = top.v[k];
+                sh.i[t0 * nsel + lane + 32 * k] = top.i[k];
+            }
+    }
+    cluster.sync();
+
+    if (rank == 0) {
+        if (tid < K) {
+            double lse = 0.0;     // finished beams: the value is the score
+            if (!(bc.done && bc.done[(long long)req * K + tid])) {
+                float m = -INFINITY;
+                for (int q = 0; q < CS; ++q)
+                    m = fmaxf(m, cluster.map_shared_rank(&sh, q)->max[tid * wpr]);
+                double s = 0.0;
+                for (int q = 0; q < CS; ++q) {
+                    const BeamShared* o = cluster.map_shared_rank(&sh, q);
+                    const float mq = o->max[tid * wpr];
+                    if (mq != -INFINITY) s += o->sum[tid * wpr] * exp((double)mq - (double)m);
+                }
+                lse = (double)m + log(s);
+            }
+            sh.lse[tid] = lse;
+        }
+        __syncthreads();
+        TopList<double, KP> best;
+        best.clear(nsel);
+        for (int li = warp; li < K * CS; li += kBWarps) {
+            const int q = li / K, row = li - q * K;
+            const BeamShared* o = cluster.map_shared_rank(&sh, q);
+            const double sc = (double)__ldg(bc.scores + (long long)req * K + row);
+            const double lse = sh.lse[row];
+#pragma unroll
+            for (int k = 0; k < KP; ++k) {
+                const int e = lane + 32 * k;
+                const bool has = e < nsel;
+                const int i = has ? o->i[row * wpr * nsel + e] : 0x7fffffff;
+                const double val = i == 0x7fffffff
+                    ? -INFINITY : sc + ((double)o->v[row * wpr * nsel + e] - lse);
+                // NaN (a score or a row without a finite sum) is never better
+                best.offer(val, val > -INFINITY ? row * V + i : 0x7fffffff);
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < KP; ++k)
+            if (lane + 32 * k < nsel) {
+                fin.v[warp * nsel + lane + 32 * k] = best.v[k];
+                fin.i[warp * nsel + lane + 32 * k] = best.i[k];
+            }
+        __syncthreads();
+        if (warp == 0) {
+            for (int w = 1; w < kBWarps; ++w) {
+#pragma unroll
+                for (int k = 0; k < KP; ++k) {
+                    const int e = lane + 32 * k;
+                    const bool has = e < nsel;
+                    best.offer(has ? fin.v[w * nsel + e] : -INFINITY,
+                               has ? fin.i[w * nsel + e] : 0x7fffffff);
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < KP; ++k) {
+                const int e = lane + 32 * k;
+                if (e < nsel) {
+                    const long long at = (long long)req * nsel + e;
+                    const bool none = best.i[k] == 0x7fffffff;
+                    bc.out_score[at] = none ? -INFINITY : (float)best.v[k];
+                    bc.out_parent[at] = none ? -1 : best.i[k] / V;
+                    bc.out_token[at] = none ? -1 : best.i[k] % V;
+                }
+            }
+        }
+    }
+    cluster.sync();   // no block leaves while its lists may be read
+}
+
+template <int TYPE, int KP>
+cudaError_t launch_one(const BeamCall& bc, int cs, cudaStream_t st)
+{
+    auto kern = beam_kernel<TYPE, KP>;
+    constexpr int smem = (int)(sizeof(BeamShared) + sizeof(FinalShared));
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(bc.batch * cs));
+    cfg.blockDim = dim3(kBThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)cs;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, bc);
+}
+
+}  // namespace
+
+cudaError_t launch_beam(const BeamCall& bc, cudaStream_t st)
+{
+    // Blocks per request: as many (up to the portable cluster size) as keep
+    // the batch within two blocks per SM and leave every warp a vector.
+    const int vec = bc.type == SSQ_T_F32 ? 4 : 8;
+    const long long vectors = (long long)bc.beams * bc.vocab / vec;
+    int cs = 1;
+    while (cs < 8 && (long long)bc.batch * cs * 2 <= 2 * kSMs
+           && vectors >= (long long)cs * 2 * kBThreads)
+        cs *= 2;
+    const bool two = bc.nsel > 32;
+    switch (bc.type) {
+    case SSQ_T_BF16:
+        return two ? launch_one<SSQ_T_BF16, 2>(bc, cs, st) : launch_one<SSQ_T_BF16, 1>(bc, cs, st);
+    case SSQ_T_F16:
+        return two ? launch_one<SSQ_T_F16, 2>(bc, cs, st) : launch_one<SSQ_T_F16, 1>(bc, cs, st);
+    default:
+        return two ? launch_one<SSQ_T_F32, 2>(bc, cs, st) : launch_one<SSQ_T_F32, 1>(bc, cs, st);
+    }
+}
+
+}  // namespace ssq

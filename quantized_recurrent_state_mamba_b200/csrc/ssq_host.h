@@ -1,0 +1,34 @@
+// ssq_host.h -- host helpers of the entry points, defined in ssq_api.cu:
+// error reporting, argument checks and the device view of a pool.
+#pragma once
+
+#include <stddef.h>
+
+#include "ssq.h"
+#include "ssq_params.h"
+
+namespace ssq {
+namespace host {
+
+// Record the one-line reason that ssq_last_error_detail returns; gives s back.
+ssq_status fail(ssq_status s, const char* fmt, ...);
+ssq_status cuda_fail(cudaError_t e, const char* what);
+bool aligned(const void* p, size_t a);
+// p present and aligned.
+ssq_status need(const void* p, const char* name, size_t align);
+// Validate a config and fill the layout (and the region order of the heads).
+ssq_status layout_of(const ssq_config* cfg, ssq_layout* L, int32_t* perm);
+ssq_status damp_layout_of(const ssq_damp_config* c, ssq_damp_layout* L);
+ssq_status make_pool_view(const ssq_config* cfg, void* pool, PoolView* pv, ssq_layout* L);
+// Common checks of (slot_idx, batch, layer range).
+ssq_status check_batch(const ssq_config* cfg, const int32_t* slot_idx, int batch, int layer0,
+                       int nl);
+
+}  // namespace host
+}  // namespace ssq
+
+#define SSQ_TRY(x)                         \
+    do {                                   \
+        ssq_status _s = (x);               \
+        if (_s != SSQ_OK) return _s;       \
+    } while (0)

@@ -1,0 +1,60 @@
+// ssq_ragged.h -- launch parameters of ssq_prefill_ragged.
+#pragma once
+
+#include "ssq_params.h"
+#include "ssq_serve.h"
+
+namespace ssq {
+
+struct RaggedCall {
+    const int32_t* slot_idx;   // [batch] or null (identity)
+    const int32_t* cu;         // [batch+1]
+    const uint8_t* fresh;      // [batch] or null
+    int batch, layer, max_len;
+    int chunk_min;             // runs of at least this many tokens go through chunks
+    int chunked;               // the chunk kernel runs beside the token kernel
+    long long total;
+    int type;                  // ssq_dtype
+    const void *x, *B, *C;
+    const float *dt, *A, *D;
+    void* y;
+    long long xs, Bs, Cs, dts, ys;   // token strides in elements
+    // chunk kernel: segments of seg_chunks chunks; states [batch][nseg][H][P][N]
+    // and decays [batch][nseg][H] of the workspace (nseg > 1)
+    int nseg, seg_chunks;
+    float* ws_state;
+    float* ws_decay;
+};
+
+// One request as the kernels see it; ok is false where it is skipped.
+struct Run {
+    int slot, t0, len;
+    bool fresh, ok;
+};
+
+// Every thread of a block calls this; `report` (one thread of one block per
+// request) records why a request is skipped.
+__device__ __forceinline__ Run ragged_run(const PoolView& pv, const RaggedCall& rc, int b,
+                                          bool report)
+{
+    Run r;
+    r.slot = rc.slot_idx ? __ldg(rc.slot_idx + b) : b;
+    r.t0 = __ldg(rc.cu + b);
+    const int t1 = __ldg(rc.cu + b + 1);
+    r.fresh = rc.fresh && __ldg(rc.fresh + b) != 0;
+    const bool tok_ok = r.t0 >= 0 && t1 >= r.t0 && t1 <= rc.total && t1 - r.t0 <= rc.max_len;
+    const bool slot_ok = r.slot >= 0 && r.slot < pv.n_slots;
+    r.len = tok_ok ? t1 - r.t0 : 0;
+    r.ok = tok_ok && slot_ok;
+    if (report && !r.ok)
+        atomicOr(reinterpret_cast<unsigned*>(pv.pool),
+                 (tok_ok ? 0u : SSQ_DEVERR_TOKENS) | (slot_ok ? 0u : SSQ_DEVERR_SLOT));
+    return r;
+}
+
+// Token by token (ssq_ragged.cu), and in chunks on the tensor cores
+// (ssq_chunk.cu).
+cudaError_t launch_ragged_tokens(const PoolView& pv, const RaggedCall& rc, int fmt,
+                                 cudaStream_t st);
+
+}  // namespace ssq

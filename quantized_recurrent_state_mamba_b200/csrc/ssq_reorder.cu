@@ -1,0 +1,201 @@
+// ssq_reorder.cu -- ssq_pool_reorder: the slots of a request's beams take
+// their parents' states, in place.
+//
+// A reordering moves bytes: it is bound by HBM, and its floor is each parent
+// that some other beam takes read once and each slot that changes written
+// once.  A block takes one chunk (up to 16 KB) of the slots of one request at
+// a time: it brings that chunk of every parent needed into shared memory with
+// bulk copies, waits, and copies it out to every slot that changes.  All
+// reads of a chunk come before its writes and chunks do not overlap, so the
+// permutation needs no second buffer in global memory.  Four stages keep
+// loads and stores of different chunks in flight; one warp per block issues
+// everything (lane l the copies of beams l and l + 32).
+#include "ssq_common.cuh"
+#include "ssq_pipe.cuh"
+#include "ssq_serve_params.h"
+
+namespace ssq {
+
+namespace {
+
+constexpr int kStages = 4;
+constexpr int kStageBudget = 48 * 1024;   // bytes of a stage
+
+struct Item {
+    long long off;     // offset within a slot
+    unsigned bytes;
+};
+
+__device__ __forceinline__ Item item_at(const ReorderCall& rc, long long c)
+{
+    Item it;
+    int r = 0;
+    while (r < 2 && c >= rc.chunks[r]) c -= rc.chunks[r++];
+    const long long at = c * rc.chunk_bytes;
+    it.off = rc.range_off[r] + at;
+    it.bytes = (unsigned)min((long long)rc.chunk_bytes, rc.range_bytes[r] - at);
+    return it;
+}
+
+// The request as lane l sees it, beams k = l and l + 32.
+struct Group {
+    long long base[2];   // the beam's slot
+    int from[2];         // stage position of the state it takes, -1: none
+    int at[2];           // stage position of its own state, -1: nobody takes it
+    int nsrc;
+    bool ok;
+};
+
+__device__ __forceinline__ Group load_group(const ReorderCall& rc, int req)
+{
+    const unsigned full = 0xffffffffu;
+    const int lane = threadIdx.x;
+    Group g;
+    int slot[2], par[2];
+    unsigned err = 0;
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+        const int k = lane + 32 * s;
+        slot[s] = -1 - k;              // distinct and outside the pool
+        par[s] = -1;
+        if (k < rc.beams) {
+            const long long i = (long long)req * rc.beams + k;
+            slot[s] = rc.slot_idx ? __ldg(rc.slot_idx + i) : (int)i;
+            par[s] = __ldg(rc.parent + i);
+            if (slot[s] < 0 || slot[s] >= rc.n_slots) err |= SSQ_DEVERR_SLOT;
+            if (par[s] < -1 || par[s] >= rc.beams) err |= SSQ_DEVERR_PARENT;
+        }
+        if (par[s] == k) par[s] = -1;  // stays where it is
+        g.base[s] = rc.header_bytes + (long long)slot[s] * rc.slot_bytes;
+    }
+    // two beams in one slot, and which beams are taken by another
+    bool taken[2] = {false, false};
+    for (int k = 0; k < rc.beams; ++k) {
+        const int sk = __shfl_sync(full, k < 32 ? slot[0] : slot[1], k & 31);
+        const int pk = __shfl_sync(full, k < 32 ? par[0] : par[1], k & 31);
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            if (lane + 32 * s != k && slot[s] == sk) err |= SSQ_DEVERR_PARENT;
+            if (pk == lane + 32 * s) taken[s] = true;
+        }
+    }
+    err = __reduce_or_sync(full, err);
+    g.ok = err == 0;
+    if (err && lane == 0) atomicOr(reinterpret_cast<unsigned*>(rc.pool), err);
+    const unsigned m0 = __ballot_sync(full, taken[0]), m1 = __ballot_sync(full, taken[1]);
+    const unsigned below = (1u << lane) - 1;
+    g.at[0] = taken[0] ? __popc(m0 & below) : -1;
+    g.at[1] = taken[1] ? __popc(m0) + __popc(m1 & below) : -1;
+    g.nsrc = g.ok ? __popc(m0) + __popc(m1) : 0;
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+        const int p = par[s] & 63;
+        const int a0 = __shfl_sync(full, g.at[0], p & 31), a1 = __shfl_sync(full, g.at[1], p & 31);
+        g.from[s] = par[s] < 0 ? -1 : (p < 32 ? a0 : a1);
+    }
+    return g;
+}
+
+__global__ void __launch_bounds__(32)
+reorder_kernel(const __grid_constant__ ReorderCall rc)
+{
+    extern __shared__ __align__(128) unsigned char smem[];
+    __shared__ __align__(8) uint64_t full[kStages];
+    const int lane = threadIdx.x;
+    if (lane == 0) {
+        for (int s = 0; s < kStages; ++s) mbar_init(&full[s], 1);
+        fence_proxy_async();
+    }
+    __syncwarp();
+    const long long per = rc.chunks[0] + rc.chunks[1] + rc.chunks[2];
+    const long long items = per * rc.batch;
+    // contiguous shares, so that a block meets few requests
+    const long long lo = items * blockIdx.x / gridDim.x;
+    const long long hi = items * (blockIdx.x + 1) / gridDim.x;
+    const long long stage_bytes = (long long)rc.chunk_bytes * rc.beams;
+
+    int lreq = -1, sreq = -1;          // the requests whose groups are held
+    Group lg = {}, sg = {};
+    unsigned loading = 0, phase = 0;   // stages with a load to wait for; their parities
+    bool live = true;
+    long long next = lo;               // the next item to load
+    for (long long it = lo; it < hi; ++it) {
+        // Loads, up to kStages - 2 items ahead: item `next` takes the stage
+        // of an item two or more before `it`, whose stores have read it once
+        // all but the newest group have.
+        for (; next < hi && next < it + kStages - 1; ++next) {
+            const int req = (int)(next / per);
+            if (req != lreq) {
+                lg = load_group(rc, req);
+                lreq = req;
+            }
+            if (lg.nsrc == 0) continue;
+            bulk_wait_read<1>();
+            __syncwarp();
+            const int st = (int)((next - lo) % kStages);
+            const Item im = item_at(rc, next - (long long)req * per);
+            if (lane == 0) mbar_arrive_tx(&full[st], im.bytes * (unsigned)lg.nsrc);
+            __syncwarp();
+            loading |= 1u << st;
+#pragma unroll
+            for (int s = 0; s < 2; ++s)
+                if (lg.at[s] >= 0)
+                    bulk_g2s(smem + st * stage_bytes + (long long)lg.at[s] * rc.chunk_bytes,
+                             rc.pool + lg.base[s] + im.off, im.bytes, &full[st]);
+        }
+        const int req = (int)(it / per);
+        if (req != sreq) {
+            sg = req == lreq ? lg : load_group(rc, req);
+            sreq = req;
+        }
+        if (sg.nsrc != 0) {
+            const int st = (int)((it - lo) % kStages);
+            live = __all_sync(0xffffffffu, mbar_wait_suspend(&full[st], (phase >> st) & 1u));
+            if (!live) break;
+            phase ^= 1u << st;
+            loading &= ~(1u << st);
+            const Item im = item_at(rc, it - (long long)req * per);
+#pragma unroll
+            for (int s = 0; s < 2; ++s)
+                if (sg.from[s] >= 0)
+                    bulk_s2g(rc.pool + sg.base[s] + im.off,
+                             smem + st * stage_bytes + (long long)sg.from[s] * rc.chunk_bytes,
+                             im.bytes);
+        }
+        bulk_commit();
+    }
+    if (!live) {
+        // a load did not land in time: report it, and give those in flight
+        // as long again before the block's shared memory goes away
+        if (lane == 0)
+            atomicOr(reinterpret_cast<unsigned*>(rc.pool), SSQ_DEVERR_TIMEOUT);
+        for (int st = 0; st < kStages; ++st)
+            if (loading >> st & 1u) mbar_wait_suspend(&full[st], (phase >> st) & 1u);
+    }
+    bulk_wait<0>();
+}
+
+}  // namespace
+
+cudaError_t launch_reorder(ReorderCall rc, cudaStream_t st)
+{
+    // the largest power of two per beam, up to 16 KB, that fits a stage
+    int chunk = 16 * 1024;
+    while (chunk * rc.beams > kStageBudget) chunk /= 2;
+    rc.chunk_bytes = chunk;
+    long long per = 0;
+    for (int r = 0; r < 3; ++r) {
+        rc.chunks[r] = (rc.range_bytes[r] + chunk - 1) / chunk;
+        per += rc.chunks[r];
+    }
+    const long long items = per * rc.batch;
+    const int smem = kStages * chunk * rc.beams;
+    cudaError_t e = cudaFuncSetAttribute(reorder_kernel,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    const unsigned grid = (unsigned)(items < kSMs ? items : kSMs);
+    reorder_kernel<<<grid, 32, smem, st>>>(rc);
+    return cudaGetLastError();
+}
+
+}  // namespace ssq

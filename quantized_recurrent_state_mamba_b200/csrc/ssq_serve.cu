@@ -1,0 +1,247 @@
+// ssq_serve.cu -- the extern "C" entry points of ssq_serve.h: argument
+// validation and dispatch to the kernel launchers.
+#include <cstring>
+
+#include "ssq_host.h"
+#include "ssq_ragged.h"
+#include "ssq_serve.h"
+#include "ssq_serve_params.h"
+
+using namespace ssq::host;
+
+namespace {
+
+size_t elem_bytes(ssq_dtype t) { return t == SSQ_T_F32 ? 4 : 2; }
+
+ssq_status check_type(ssq_dtype t)
+{
+    if (t != SSQ_T_BF16 && t != SSQ_T_F16 && t != SSQ_T_F32)
+        return fail(SSQ_ERR_INVALID_ARG, "unknown element type %d", (int)t);
+    return SSQ_OK;
+}
+
+ssq_status check_stride(const char* name, long long stride, long long least)
+{
+    if (stride < least)
+        return fail(SSQ_ERR_INVALID_ARG, "%s stride %lld < %lld", name, stride, least);
+    // byte offsets of a token stay far inside 64 bits
+    if (stride > (1LL << 31))
+        return fail(SSQ_ERR_INVALID_ARG, "%s stride %lld > 2^31", name, stride);
+    return SSQ_OK;
+}
+
+ssq_status check_beams(int batch, int beams)
+{
+    if (batch < 0) return fail(SSQ_ERR_INVALID_ARG, "batch %d < 0", batch);
+    if (beams < 1) return fail(SSQ_ERR_INVALID_ARG, "beams %d < 1", beams);
+    if (beams > SSQ_MAX_BEAMS)
+        return fail(SSQ_ERR_UNSUPPORTED, "beams %d > %d", beams, SSQ_MAX_BEAMS);
+    return SSQ_OK;
+}
+
+ssq_status check_reorder(int n_layers, int n_slots, const int32_t* slot_idx, int batch, int beams,
+                         const int32_t* parent, int layer0, int nl)
+{
+    SSQ_TRY(check_beams(batch, beams));
+    if (nl < 1) return fail(SSQ_ERR_INVALID_ARG, "nl %d < 1", nl);
+    if (layer0 < 0 || (long long)layer0 + nl > n_layers)
+        return fail(SSQ_ERR_INVALID_ARG, "layers [%d, %d) outside [0, %d)", layer0,
+                    layer0 + nl, n_layers);
+    if ((long long)batch * beams > n_slots)
+        return fail(SSQ_ERR_INVALID_ARG, "%lld beams > n_slots %d", (long long)batch * beams,
+                    n_slots);
+    if (slot_idx && !aligned(slot_idx, 4))
+        return fail(SSQ_ERR_ALIGNMENT, "slot_idx not 4-byte aligned");
+    return batch > 0 ? need(parent, "parent", 4) : SSQ_OK;
+}
+
+ssq_status run_reorder(const ssq::ReorderCall& rc, cudaStream_t stream)
+{
+    if (rc.batch == 0) return SSQ_OK;
+    const cudaError_t e = ssq::launch_reorder(rc, stream);
+    if (e != cudaSuccess) return cuda_fail(e, "reorder launch");
+    return SSQ_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+ssq_status ssq_prefill_ragged_workspace(const ssq_config* cfg, int batch, int max_len,
+                                        size_t* bytes)
+{
+    ssq_layout L;
+    SSQ_TRY(layout_of(cfg, &L, nullptr));
+    if (batch < 0) return fail(SSQ_ERR_INVALID_ARG, "batch %d < 0", batch);
+    if (max_len < 0) return fail(SSQ_ERR_INVALID_ARG, "max_len %d < 0", max_len);
+    if (!bytes) return fail(SSQ_ERR_INVALID_ARG, "bytes is NULL");
+    *bytes = 0;
+    return SSQ_OK;
+}
+
+ssq_status ssq_prefill_ragged(const ssq_config* cfg, void* pool, const int32_t* slot_idx,
+                              int batch, int layer, const int32_t* cu_tokens, int max_len,
+                              const uint8_t* fresh, const ssq_tokens* tok, const float* A,
+                              const float* D, void* workspace, size_t workspace_bytes,
+                              cudaStream_t stream)
+{
+    ssq::PoolView pv;
+    ssq_layout L;
+    SSQ_TRY(make_pool_view(cfg, pool, &pv, &L));
+    SSQ_TRY(check_batch(cfg, slot_idx, batch, layer, 1));
+    if (max_len < 0) return fail(SSQ_ERR_INVALID_ARG, "max_len %d < 0", max_len);
+    SSQ_TRY(need(cu_tokens, "cu_tokens", 4));
+    if (!tok) return fail(SSQ_ERR_INVALID_ARG, "tok is NULL");
+    SSQ_TRY(check_type(tok->type));
+    if (tok->total < 0 || tok->total > 0x7fffffffLL)
+        return fail(SSQ_ERR_INVALID_ARG, "total %lld outside [0, 2^31)", tok->total);
+    const long long HP = (long long)cfg->nheads * cfg->headdim;
+    const long long GN = (long long)cfg->ngroups * cfg->d_state;
+    SSQ_TRY(check_stride("x", tok->x_stride, HP));
+    SSQ_TRY(check_stride("B", tok->B_stride, GN));
+    SSQ_TRY(check_stride("C", tok->C_stride, GN));
+    SSQ_TRY(check_stride("dt", tok->dt_stride, cfg->nheads));
+    SSQ_TRY(check_stride("y", tok->y_stride, HP));
+    const size_t eb = elem_bytes(tok->type);
+    if (tok->total > 0) {
+        SSQ_TRY(need(tok->x, "x", eb));
+        SSQ_TRY(need(tok->B, "B", eb));
+        SSQ_TRY(need(tok->C, "C", eb));
+        SSQ_TRY(need(tok->dt, "dt", 4));
+        SSQ_TRY(need(tok->y, "y", eb));
+    }
+    SSQ_TRY(need(A, "A", 4));
+    SSQ_TRY(need(D, "D", 4));
+    size_t want = 0;
+    SSQ_TRY(ssq_prefill_ragged_workspace(cfg, batch, max_len, &want));
+    if (want > 0) {
+        SSQ_TRY(need(workspace, "workspace", 256));
+        if (workspace_bytes < want)
+            return fail(SSQ_ERR_INVALID_ARG, "workspace of %zu bytes, need %zu", workspace_bytes,
+                        want);
+    }
+    if (batch == 0) return SSQ_OK;
+    ssq::RaggedCall rc;
+    memset(&rc, 0, sizeof(rc));
+    rc.slot_idx = slot_idx;
+    rc.cu = cu_tokens;
+    rc.fresh = fresh;
+    rc.batch = batch;
+    rc.layer = layer;
+    rc.max_len = max_len;
+    rc.chunk_min = 0x7fffffff;
+    rc.total = tok->total;
+    rc.type = (int)tok->type;
+    rc.x = tok->x;
+    rc.B = tok->B;
+    rc.C = tok->C;
+    rc.dt = tok->dt;
+    rc.A = A;
+    rc.D = D;
+    rc.y = tok->y;
+    rc.xs = tok->x_stride;
+    rc.Bs = tok->B_stride;
+    rc.Cs = tok->C_stride;
+    rc.dts = tok->dt_stride;
+    rc.ys = tok->y_stride;
+    const cudaError_t e = ssq::launch_ragged_tokens(pv, rc, (int)cfg->fmt, stream);
+    if (e != cudaSuccess) return cuda_fail(e, "prefill_ragged launch");
+    return SSQ_OK;
+}
+
+ssq_status ssq_beam_select(int batch, int beams, int vocab, ssq_dtype type, const void* logits,
+                           long long logits_stride, const float* scores, const uint8_t* done,
+                           int done_token, int nsel, float* out_score, int32_t* out_parent,
+                           int32_t* out_token, cudaStream_t stream)
+{
+    SSQ_TRY(check_beams(batch, beams));
+    if (vocab < 1) return fail(SSQ_ERR_INVALID_ARG, "vocab %d < 1", vocab);
+    if ((long long)beams * vocab > 0x7fffffffLL - 1)
+        return fail(SSQ_ERR_UNSUPPORTED, "beams*vocab %lld not below 2^31 - 1",
+                    (long long)beams * vocab);
+    SSQ_TRY(check_type(type));
+    SSQ_TRY(check_stride("logits", logits_stride, vocab));
+    if (nsel < 1) return fail(SSQ_ERR_INVALID_ARG, "nsel %d < 1", nsel);
+    if (nsel > SSQ_MAX_BEAMS)
+        return fail(SSQ_ERR_UNSUPPORTED, "nsel %d > %d", nsel, SSQ_MAX_BEAMS);
+    if (done && (done_token < 0 || done_token >= vocab))
+        return fail(SSQ_ERR_INVALID_ARG, "done_token %d outside [0, %d)", done_token, vocab);
+    if ((long long)batch * 8 > 0x7fffffffLL)
+        return fail(SSQ_ERR_UNSUPPORTED, "batch %d too large", batch);
+    if (batch == 0) return SSQ_OK;
+    SSQ_TRY(need(logits, "logits", elem_bytes(type)));
+    SSQ_TRY(need(scores, "scores", 4));
+    SSQ_TRY(need(out_score, "out_score", 4));
+    SSQ_TRY(need(out_parent, "out_parent", 4));
+    SSQ_TRY(need(out_token, "out_token", 4));
+    ssq::BeamCall bc;
+    memset(&bc, 0, sizeof(bc));
+    bc.batch = batch;
+    bc.beams = beams;
+    bc.vocab = vocab;
+    bc.nsel = nsel;
+    bc.done_token = done_token;
+    bc.type = (int)type;
+    bc.logits = logits;
+    bc.stride = logits_stride;
+    bc.scores = scores;
+    bc.done = done;
+    bc.out_score = out_score;
+    bc.out_parent = out_parent;
+    bc.out_token = out_token;
+    const cudaError_t e = ssq::launch_beam(bc, stream);
+    if (e != cudaSuccess) return cuda_fail(e, "beam_select launch");
+    return SSQ_OK;
+}
+
+ssq_status ssq_pool_reorder(const ssq_config* cfg, void* pool, const int32_t* slot_idx, int batch,
+                            int beams, const int32_t* parent, int layer0, int nl,
+                            cudaStream_t stream)
+{
+    ssq_layout L;
+    SSQ_TRY(layout_of(cfg, &L, nullptr));
+    SSQ_TRY(need(pool, "pool", SSQ_POOL_ALIGN));
+    SSQ_TRY(check_reorder(cfg->n_layers, cfg->n_slots, slot_idx, batch, beams, parent, layer0, nl));
+    ssq::ReorderCall rc;
+    memset(&rc, 0, sizeof(rc));
+    rc.pool = static_cast<uint8_t*>(pool);
+    rc.header_bytes = (long long)L.header_bytes;
+    rc.slot_bytes = (long long)L.slot_bytes;
+    const size_t off[3] = {L.codes_off, L.meta_off, L.fp_off};
+    const size_t lay[3] = {L.codes_layer_bytes, L.meta_layer_bytes, L.fp_layer_bytes};
+    for (int r = 0; r < 3; ++r) {
+        rc.range_off[r] = (long long)(off[r] + lay[r] * (size_t)layer0);
+        rc.range_bytes[r] = (long long)(lay[r] * (size_t)nl);
+    }
+    rc.n_slots = cfg->n_slots;
+    rc.batch = batch;
+    rc.beams = beams;
+    rc.slot_idx = slot_idx;
+    rc.parent = parent;
+    return run_reorder(rc, stream);
+}
+
+ssq_status ssq_damp_pool_reorder(const ssq_damp_config* cfg, void* pool, const int32_t* slot_idx,
+                                 int batch, int beams, const int32_t* parent, int layer0, int nl,
+                                 cudaStream_t stream)
+{
+    ssq_damp_layout L;
+    SSQ_TRY(damp_layout_of(cfg, &L));
+    SSQ_TRY(need(pool, "pool", SSQ_POOL_ALIGN));
+    SSQ_TRY(check_reorder(cfg->n_layers, cfg->n_slots, slot_idx, batch, beams, parent, layer0, nl));
+    ssq::ReorderCall rc;
+    memset(&rc, 0, sizeof(rc));
+    rc.pool = static_cast<uint8_t*>(pool);
+    rc.header_bytes = (long long)L.header_bytes;
+    rc.slot_bytes = (long long)L.slot_bytes;
+    rc.range_off[0] = (long long)(L.layer_bytes * (size_t)layer0);
+    rc.range_bytes[0] = (long long)(L.layer_bytes * (size_t)nl);
+    rc.n_slots = cfg->n_slots;
+    rc.batch = batch;
+    rc.beams = beams;
+    rc.slot_idx = slot_idx;
+    rc.parent = parent;
+    return run_reorder(rc, stream);
+}
+
+}  // extern "C"

@@ -1,0 +1,36 @@
+// ssq_serve_params.h -- launch parameters of the beam entry points.
+#pragma once
+
+#include "ssq_params.h"
+#include "ssq_serve.h"
+
+namespace ssq {
+
+// SMs of the one GPU that the library is built for (B200).
+constexpr int kSMs = 148;
+
+struct BeamCall {
+    int batch, beams, vocab, nsel, done_token;
+    int type;                 // ssq_dtype
+    const void* logits;
+    long long stride;         // elements between the rows of two beams
+    const float* scores;
+    const uint8_t* done;
+    float* out_score;
+    int32_t *out_parent, *out_token;
+};
+cudaError_t launch_beam(const BeamCall& bc, cudaStream_t st);
+
+// Byte ranges that a reordering moves inside every slot (256-byte multiples).
+struct ReorderCall {
+    uint8_t* pool;
+    long long header_bytes, slot_bytes;
+    long long range_off[3], range_bytes[3];
+    int n_slots, batch, beams;
+    const int32_t *slot_idx, *parent;
+    int chunk_bytes;          // bytes of a slot that one stage holds per beam
+    long long chunks[3];      // chunks of each range
+};
+cudaError_t launch_reorder(ReorderCall rc, cudaStream_t st);
+
+}  // namespace ssq

@@ -1,4 +1,4 @@
-"""Thin Python binding over libssq (include/ssq.h).
+"""Thin Python binding over libssq (include/ssq.h, include/ssq_serve.h).
 
 Argument marshalling only: every function checks that the tensors it is given
 are CUDA tensors of the documented dtype, contiguity and size (the C ABI sees
@@ -31,9 +31,14 @@ SSQ_DEVERR_SLOT = 0x1
 SSQ_DEVERR_NONFINITE = 0x2
 SSQ_DEVERR_TIMEOUT = 0x4
 SSQ_DEVERR_CHANNEL = 0x8
+SSQ_DEVERR_TOKENS = 0x10
+SSQ_DEVERR_PARENT = 0x20
 SSQ_MAX_HEADS = 512
 SSQ_POOL_HEADER_BYTES = 256
 SSQ_POOL_ALIGN = 256
+SSQ_MAX_BEAMS = 64
+SSQ_T_BF16, SSQ_T_F16, SSQ_T_F32 = range(3)
+_ACT_TYPES = {torch.bfloat16: SSQ_T_BF16, torch.float16: SSQ_T_F16, torch.float32: SSQ_T_F32}
 
 
 class SsqError(RuntimeError):
@@ -68,6 +73,12 @@ class ssq_damp_layout(ctypes.Structure):
         "codes_off", "meta_off")] + [("bits_per_value", ctypes.c_double)]
 
 
+class ssq_tokens(ctypes.Structure):
+    _fields_ = [("type", ctypes.c_int)] + [(n, ctypes.c_void_p) for n in (
+        "x", "B", "C", "dt", "y")] + [(n, ctypes.c_longlong) for n in (
+            "x_stride", "B_stride", "C_stride", "dt_stride", "y_stride", "total")]
+
+
 _P = ctypes.c_void_p
 _CFG = ctypes.POINTER(ssq_config)
 _I = ctypes.c_int
@@ -93,7 +104,15 @@ _lib.ssq_damp_dequantize.argtypes = [_DCFG, _P, _P, _P, _I, _I, _I, _P, _P]
 _lib.ssq_damp_decode_step.argtypes = [_DCFG, _P, _P, _P, _I, _I, _I] + [_P] * 7 + [_P]
 _lib.ssq_damp_pool_error.argtypes = [_DCFG, _P, ctypes.POINTER(ctypes.c_uint32), _P]
 _lib.ssq_test_hooks.argtypes = [_I, ctypes.c_longlong]
-for _f in ("ssq_test_hooks", "ssq_pool_layout", "ssq_pool_init", "ssq_pool_error", "ssq_quantize_rows",
+_lib.ssq_prefill_ragged_workspace.argtypes = [_CFG, _I, _I, ctypes.POINTER(ctypes.c_size_t)]
+_lib.ssq_prefill_ragged.argtypes = [_CFG, _P, _P, _I, _I, _P, _I, _P,
+                                    ctypes.POINTER(ssq_tokens), _P, _P, _P, ctypes.c_size_t, _P]
+_lib.ssq_beam_select.argtypes = [_I, _I, _I, _I, _P, ctypes.c_longlong, _P, _P, _I, _I, _P, _P,
+                                 _P, _P]
+_lib.ssq_pool_reorder.argtypes = [_CFG, _P, _P, _I, _I, _P, _I, _I, _P]
+_lib.ssq_damp_pool_reorder.argtypes = [_DCFG, _P, _P, _I, _I, _P, _I, _I, _P]
+for _f in ("ssq_prefill_ragged_workspace", "ssq_prefill_ragged", "ssq_beam_select",
+           "ssq_pool_reorder", "ssq_damp_pool_reorder", "ssq_test_hooks", "ssq_pool_layout", "ssq_pool_init", "ssq_pool_error", "ssq_quantize_rows",
            "ssq_dequantize_rows", "ssq_decode_step", "ssq_scan", "ssq_prefill",
            "ssq_decode_step_sr", "ssq_scan_sr", "ssq_decode_diag", "ssq_damp_pool_layout",
            "ssq_damp_quantize", "ssq_damp_dequantize", "ssq_damp_decode_step",
@@ -379,6 +398,158 @@ def ssq_damp_pool_error(cfg: DampConfig, pool, stream=None) -> int:
     _check(_lib.ssq_damp_pool_error(cfg.ref, _ptr(pool, "pool", torch.uint8, L["pool_bytes"]),
                                     ctypes.byref(v), _stream(stream)))
     return int(v.value)
+
+
+# ---------------------------------------------------------------------------
+# Ragged prompts, beams (include/ssq_serve.h)
+# ---------------------------------------------------------------------------
+
+def _on(device, **tensors):
+    """All given tensors live on `device`."""
+    for name, t in tensors.items():
+        if isinstance(t, torch.Tensor) and t.device != device:
+            raise ValueError(f"{name}: on {t.device}, the pool or logits on {device}")
+
+
+def _token_ptr(t, name, dtype, total, shape):
+    """A [total, *shape] tensor whose entries of one token are contiguous: its
+    pointer and the stride from token to token."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name}: expected a CUDA tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+    if tuple(t.shape) != (total, *shape):
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, need {(total, *shape)}")
+    inner = 1
+    for k in range(len(shape) - 1, -1, -1):
+        if shape[k] > 1 and t.stride(k + 1) != inner:
+            raise ValueError(f"{name}: the entries of one token must be contiguous")
+        inner *= shape[k]
+    return t.data_ptr(), (t.stride(0) if total > 1 else inner)
+
+
+def ssq_prefill_ragged_workspace(cfg: Config, batch, max_len) -> int:
+    """Bytes of workspace that ssq_prefill_ragged needs (0: none)."""
+    v = ctypes.c_size_t(0)
+    _check(_lib.ssq_prefill_ragged_workspace(cfg.ref, batch, max_len, ctypes.byref(v)))
+    return int(v.value)
+
+
+def alloc_prefill_workspace(cfg: Config, batch, max_len, device="cuda"):
+    """A workspace for ssq_prefill_ragged with up to this batch and longest
+    run, or None where none is needed."""
+    n = ssq_prefill_ragged_workspace(cfg, batch, max_len)
+    return torch.empty(n, dtype=torch.uint8, device=device) if n else None
+
+
+def ssq_prefill_ragged(cfg: Config, pool, slot_idx, batch, layer, cu_tokens, max_len, x, B, C, dt,
+                       A, D, y, fresh=None, workspace=None, stream=None):
+    """Prompts, pieces of prompts and single tokens of one layer, packed
+    without padding: request b owns tokens cu_tokens[b] .. cu_tokens[b+1]-1
+    (int32 [batch+1]).  x/y [total][H][P], B/C [total][G][N] in bfloat16,
+    float16 or float32 (token strides free), dt [total][H], A/D [H] float32;
+    fresh uint8 [batch] marks requests that start from the zero state."""
+    H, P, N, G = cfg.nheads, cfg.headdim, cfg.d_state, cfg.ngroups
+    f = torch.float32
+    pp = _pool_ptr(cfg, pool)
+    if not isinstance(x, torch.Tensor) or x.dtype not in _ACT_TYPES:
+        raise TypeError("x: expected a bfloat16, float16 or float32 tensor")
+    _on(x.device, pool=pool, slot_idx=slot_idx, cu_tokens=cu_tokens, B=B, C=C, dt=dt, A=A, D=D,
+        y=y, fresh=fresh, workspace=workspace)
+    total = x.shape[0]
+    tok = ssq_tokens()
+    tok.type = _ACT_TYPES[x.dtype]
+    tok.total = total
+    tok.x, tok.x_stride = _token_ptr(x, "x", x.dtype, total, (H, P))
+    tok.B, tok.B_stride = _token_ptr(B, "B", x.dtype, total, (G, N))
+    tok.C, tok.C_stride = _token_ptr(C, "C", x.dtype, total, (G, N))
+    tok.dt, tok.dt_stride = _token_ptr(dt, "dt", f, total, (H,))
+    tok.y, tok.y_stride = _token_ptr(y, "y", x.dtype, total, (H, P))
+    ws = 0
+    if workspace is not None:
+        if not isinstance(workspace, torch.Tensor) or not workspace.is_contiguous():
+            raise ValueError("workspace: expected a contiguous CUDA tensor")
+        ws = workspace.numel() * workspace.element_size()
+    with torch.cuda.device(x.device):
+        _check(_lib.ssq_prefill_ragged(
+            cfg.ref, pp, _slots(slot_idx, batch), batch, layer,
+            _ptr(cu_tokens, "cu_tokens", torch.int32, batch + 1), max_len,
+            _ptr(fresh, "fresh", torch.uint8, batch, allow_none=True), ctypes.byref(tok),
+            _ptr(A, "A", f, H), _ptr(D, "D", f, H),
+            workspace.data_ptr() if ws else None, ws, _stream(stream)))
+
+
+def ssq_beam_select(logits, scores, done=None, done_token=0, nsel=None, out=None, stream=None):
+    """The nsel (default: as many as beams) best continuations of each request
+    over its beams and the vocabulary: logits [batch][beams][vocab] in
+    bfloat16, float16 or float32, accumulated scores float32 [batch][beams],
+    done uint8 [batch][beams] (finished beams).  Returns (score float32,
+    parent int32, token int32), each [batch][nsel]; `out` takes such a triple
+    to write into."""
+    if not isinstance(logits, torch.Tensor) or logits.dtype not in _ACT_TYPES:
+        raise TypeError("logits: expected a bfloat16, float16 or float32 tensor")
+    if not logits.is_cuda:
+        raise ValueError("logits: expected a CUDA tensor")
+    if logits.dim() != 3:
+        raise ValueError(f"logits: {logits.dim()} dimensions, need [batch][beams][vocab]")
+    batch, beams, vocab = logits.shape
+    if vocab > 1 and logits.stride(2) != 1:
+        raise ValueError("logits: a row must be contiguous")
+    row = logits.stride(1) if beams > 1 else (logits.stride(0) if batch > 1 else vocab)
+    if beams > 1 and batch > 1 and logits.stride(0) != beams * row:
+        raise ValueError("logits: rows must be evenly spaced")
+    nsel = beams if nsel is None else int(nsel)
+    dev = logits.device
+    if out is None:
+        if nsel < 1:
+            raise ValueError(f"nsel: {nsel} < 1")
+        out = (torch.empty((batch, nsel), dtype=torch.float32, device=dev),
+               torch.empty((batch, nsel), dtype=torch.int32, device=dev),
+               torch.empty((batch, nsel), dtype=torch.int32, device=dev))
+    score, parent, token = out
+    _on(dev, scores=scores, done=done, score=score, parent=parent, token=token)
+    with torch.cuda.device(dev):
+        _check(_lib.ssq_beam_select(
+            batch, beams, vocab, _ACT_TYPES[logits.dtype], logits.data_ptr(), row,
+            _ptr(scores, "scores", torch.float32, batch * beams),
+            _ptr(done, "done", torch.uint8, batch * beams, allow_none=True), int(done_token), nsel,
+            _ptr(score, "score", torch.float32, batch * nsel),
+            _ptr(parent, "parent", torch.int32, batch * nsel),
+            _ptr(token, "token", torch.int32, batch * nsel), _stream(stream)))
+    return out
+
+
+def _beam_shape(parent):
+    if not isinstance(parent, torch.Tensor) or parent.dim() != 2:
+        raise ValueError("parent: expected an int32 tensor [batch][beams]")
+    return parent.shape
+
+
+def ssq_pool_reorder(cfg: Config, pool, slot_idx, parent, layer0, nl, stream=None):
+    """In place, for nl layers: the slot of beam k of request r takes the
+    state of the slot of its beam parent[r][k] (int32 [batch][beams]; -1
+    leaves it as it is).  slot_idx int32 [batch][beams] or None."""
+    batch, beams = _beam_shape(parent)
+    pp = _pool_ptr(cfg, pool)
+    _on(parent.device, pool=pool, slot_idx=slot_idx)
+    with torch.cuda.device(parent.device):
+        _check(_lib.ssq_pool_reorder(cfg.ref, pp, _slots(slot_idx, batch * beams), batch, beams,
+                                     _ptr(parent, "parent", torch.int32, batch * beams), layer0,
+                                     nl, _stream(stream)))
+
+
+def ssq_damp_pool_reorder(cfg: DampConfig, pool, slot_idx, parent, layer0, nl, stream=None):
+    """ssq_pool_reorder for a DAMP pool."""
+    batch, beams = _beam_shape(parent)
+    L = ssq_damp_pool_layout(cfg)
+    pp = _ptr(pool, "pool", torch.uint8, L["pool_bytes"])
+    _on(parent.device, pool=pool, slot_idx=slot_idx)
+    with torch.cuda.device(parent.device):
+        _check(_lib.ssq_damp_pool_reorder(
+            cfg.ref, pp, _slots(slot_idx, batch * beams), batch, beams,
+            _ptr(parent, "parent", torch.int32, batch * beams), layer0, nl, _stream(stream)))
 
 
 def ssq_status_string(status) -> str:
