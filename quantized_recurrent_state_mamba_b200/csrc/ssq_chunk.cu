@@ -1,0 +1,937 @@
+// ssq_chunk.cu -- ssq_prefill_ragged in chunks of 128 tokens on the tensor
+// cores.
+//
+// For one head, with a_t = dt_t*A, cs its running sum inside the chunk and S
+// the state (headdim x d_state) before it:
+//   G    = C B^T                                            (shared by heads)
+//   M_ij = G_ij exp(cs_i - cs_j) dt_j  for j <= i, else 0
+//   Y    = M X + diag(exp(cs_i)) C S^T + D X
+//   S   <- exp(cs_L) S + X^T diag(w) B,   w_j = dt_j exp(cs_L - cs_j)
+//
+// A block owns two units, a unit being 64 rows (p) of one head, both in one
+// group of B and C, and walks their chunks with the states in registers.
+// Warps 0-3 and 4-7 do the element work of one unit each, warp 8 issues the
+// tensor copies, warp 9 the products:
+//   G       [128 i x 128 j]  C and B from shared memory; TMEM
+//   Y2      [128 i x  64 p]  C times the state rounded to bf16; TMEM
+//   dS      [128 n x  64 p]  B^T times w X, the latter as the sum of two bf16
+//                            parts, so that the state sees its inputs to 16
+//                            bits and more; TMEM
+//   Y1      [128 i x  64 p]  M (bf16, written to TMEM) times X; the columns of
+//                            dS, which has been read by then
+// The running sums are kept per block of 32 tokens: with r_i the sum from the
+// start of i's block and q_j the sum behind j in its block, the decay between
+// two blocks is exp(r_i) * exp(sum of the blocks between) * exp(q_j), every
+// factor at most 1 for A <= 0, so only the diagonal blocks take an exp per
+// entry, and no large sums are subtracted from one another.
+//
+// What is past a run's end inside its last chunk belongs to other requests:
+// its x and B are zeroed in shared memory, so that nothing of it, NaN
+// included, reaches a sum.  A non-finite x_jp is taken out of the products
+// (in which 0 * NaN would reach earlier tokens) and makes y_ip, i >= j, and
+// the state's row p NaN.
+//
+// Long runs on few heads are cut into segments: a first pass computes each
+// segment's own state and decay, ssq_chunk_join turns them into the states
+// the segments start from, and the main pass runs all segments at once.
+#include <cstring>
+
+#include <cudaTypedefs.h>
+
+#include "ssq_ragged.h"
+#include "ssq_rowio.cuh"
+#include "ssq_serve_params.h"
+#include "ssq_tcgen.cuh"
+
+namespace ssq {
+
+namespace {
+
+constexpr int kL = 128;                 // tokens of a chunk
+constexpr int kPT = 64;                 // rows of a unit
+constexpr int kWg = 128;                // threads that work on a unit
+constexpr int kCThreadsTotal = 2 * kWg + 64;
+constexpr float kLog2e = 1.4426950408889634f;
+// exp(-1000) is 0 in fp32: sums of clamped steps stay finite for A = -inf
+constexpr float kStepFloor = -1000.0f;
+
+// Shared memory, from a 1024-byte aligned base.
+constexpr int kTileCB = kL * 256;       // C or B: two halves of [128][64] bf16
+constexpr int kTileX = kL * 128;        // [128][64] bf16
+constexpr int kRingCB = 3, kRingX = 3;
+constexpr int kOffX = kRingCB * kTileCB;
+constexpr int kOffXs = kOffX + kRingX * kTileX;      // two bf16 parts of w X
+constexpr int kOffS = kOffXs + 2 * kTileX;           // states in bf16, one per unit
+constexpr int kOffTail = kOffS + 2 * kTileX;
+
+struct UnitArrays {
+    float f[kL];        // dt_j exp(q_j)
+    float r2[kL];       // r_j log2(e)
+    float dt[kL];
+    float block[4];     // sums of the four blocks
+    int bad[kPT];       // first token of the chunk with a non-finite x in row p
+};
+struct Tail {
+    UnitArrays unit[2];
+    uint64_t cb_full[kRingCB], cb_empty[kRingCB], x_full[kRingX], x_empty[kRingX];
+    uint64_t xs_ready[2], ds_full[2], m_ready[2], y_full[2], g_full, g_free, drained;
+    uint32_t tmem;
+    int pos[2];         // region positions of the units' heads
+};
+constexpr int kSmemBytes = kOffTail + (int)sizeof(Tail) + 1024;
+static_assert(kSmemBytes <= 227 * 1024, "shared memory");
+
+// TMEM columns.
+constexpr int kTmemCols = 512;
+constexpr uint32_t kColG = 0;
+__host__ __device__ constexpr uint32_t col_m(int u) { return 128 + 192 * u; }
+__host__ __device__ constexpr uint32_t col_y1(int u) { return col_m(u) + 64; }   // and dS
+__host__ __device__ constexpr uint32_t col_y2(int u) { return col_m(u) + 128; }
+
+__device__ __forceinline__ void unit_sync(int u)
+{
+    asm volatile("bar.sync %0, %1;" :: "r"(1 + u), "n"(kWg) : "memory");
+}
+__device__ __forceinline__ bool unit_any(int u, bool v)
+{
+    unsigned r;
+    asm volatile("{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n"
+                 " barrier.red.or.pred q, %2, %3, p;\n selp.u32 %0, 1, 0, q;\n}\n"
+                 : "=r"(r) : "r"((unsigned)v), "r"(1 + u), "n"(kWg) : "memory");
+    return r != 0;
+}
+__device__ __forceinline__ void units_sync()
+{
+    asm volatile("bar.sync 3, %0;" :: "n"(2 * kWg) : "memory");
+}
+__device__ __forceinline__ float ex2(float x)
+{
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+// {lo, hi} rounded to bf16 in one word
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
+{
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+__device__ __forceinline__ float2 unpack_bf16(uint32_t w)
+{
+    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+__device__ __forceinline__ uint4 lds128(unsigned a)
+{
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+    return v;
+}
+__device__ __forceinline__ void sts128(unsigned a, uint4 v)
+{
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};"
+                 :: "r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+// Byte offset of 16-byte chunk c of 128-byte line `row` in the swizzle.
+__device__ __forceinline__ unsigned swz(int row, int c)
+{
+    return (unsigned)(row * 128 + ((c ^ (row & 7)) << 4));
+}
+
+// ---- the unit's 64 rows between the pool and stage[p][n] (fp32) -----------
+template <int FMT, int N>
+__device__ __noinline__ void pool_to_stage(const PoolView& pv, int slot, int layer, int pos,
+                                           int p0, float* stage, int t)
+{
+    constexpr int E = Shape<N>::E, LPR = Shape<N>::LPR;
+    const RowPlace place = place_head<FMT>(pv, slot, layer, pos);
+    const int j = t % LPR;
+    for (int r0 = 0; r0 < kPT; r0 += kWg / LPR) {
+        const int r = r0 + t / LPR;
+        float s[E];
+        row_load<FMT, N>(place, p0 + r, j, r < kPT && p0 + r < pv.P, s);
+        if (r < kPT)
+#pragma unroll
+            for (int n = 0; n < E; n += 4)
+                *reinterpret_cast<float4*>(stage + r * N + j * E + n) =
+                    make_float4(s[n], s[n + 1], s[n + 2], s[n + 3]);
+    }
+}
+template <int FMT, int N>
+__device__ __noinline__ void stage_to_pool(const PoolView& pv, int slot, int layer, int pos,
+                                           int p0, const float* stage, int t)
+{
+    constexpr int E = Shape<N>::E, LPR = Shape<N>::LPR;
+    const RowPlace place = place_head<FMT>(pv, slot, layer, pos);
+    const int j = t % LPR;
+    for (int r0 = 0; r0 < kPT; r0 += kWg / LPR) {
+        const int r = r0 + t / LPR;
+        const int rr = r < kPT ? r : 0;
+        float s[E];
+#pragma unroll
+        for (int n = 0; n < E; n += 4) {
+            const float4 v = *reinterpret_cast<const float4*>(stage + rr * N + j * E + n);
+            s[n] = v.x; s[n + 1] = v.y; s[n + 2] = v.z; s[n + 3] = v.w;
+        }
+        row_store<FMT, N>(place, p0 + r, j, r < kPT && p0 + r < pv.P, s,
+                          reinterpret_cast<uint32_t*>(pv.pool));
+    }
+}
+template <int FMT>
+__device__ __forceinline__ void unit_io(bool load, const PoolView& pv, int slot, int layer,
+                                        int pos, int p0, float* stage, int t)
+{
+    switch (pv.N) {
+    case 16: load ? pool_to_stage<FMT, 16>(pv, slot, layer, pos, p0, stage, t)
+                  : stage_to_pool<FMT, 16>(pv, slot, layer, pos, p0, stage, t); break;
+    case 32: load ? pool_to_stage<FMT, 32>(pv, slot, layer, pos, p0, stage, t)
+                  : stage_to_pool<FMT, 32>(pv, slot, layer, pos, p0, stage, t); break;
+    case 64: load ? pool_to_stage<FMT, 64>(pv, slot, layer, pos, p0, stage, t)
+                  : stage_to_pool<FMT, 64>(pv, slot, layer, pos, p0, stage, t); break;
+    default: load ? pool_to_stage<FMT, 128>(pv, slot, layer, pos, p0, stage, t)
+                  : stage_to_pool<FMT, 128>(pv, slot, layer, pos, p0, stage, t); break;
+    }
+}
+__device__ __noinline__ void unit_io_any(int fmt, bool load, const PoolView& pv, int slot,
+                                         int layer, int pos, int p0, float* stage, int t)
+{
+    switch (fmt) {
+    case SSQ_F32: unit_io<SSQ_F32>(load, pv, slot, layer, pos, p0, stage, t); break;
+    case SSQ_BF16: unit_io<SSQ_BF16>(load, pv, slot, layer, pos, p0, stage, t); break;
+    case SSQ_I8_SYM: unit_io<SSQ_I8_SYM>(load, pv, slot, layer, pos, p0, stage, t); break;
+    case SSQ_I8_ASYM: unit_io<SSQ_I8_ASYM>(load, pv, slot, layer, pos, p0, stage, t); break;
+    case SSQ_I4_SYM: unit_io<SSQ_I4_SYM>(load, pv, slot, layer, pos, p0, stage, t); break;
+    default: unit_io<SSQ_I4_ASYM>(load, pv, slot, layer, pos, p0, stage, t); break;
+    }
+}
+
+struct ChunkMaps {
+    CUtensorMap x, B, C;
+};
+
+// What a block works on.
+struct Work {
+    Run run;
+    int b, seg, nseg;        // request, segment, segments of the run
+    int c0, nc;              // chunks of the segment
+    int h[2], p0[2], nu;     // units
+    int g;
+};
+
+// ---------------------------------------------------------------------------
+// Element work of unit u: 128 threads; thread t is token t of the chunk for
+// x, M and y, and entry n = t of the state.
+// ---------------------------------------------------------------------------
+template <bool STATE>
+__device__ __forceinline__ bool unit_loop(const PoolView& pv, const RaggedCall& rc, const Work& wk,
+                                          unsigned base, Tail& tl, uint32_t tmem, int u, int t,
+                                          float (&S)[kPT], float& decay_all)
+{
+    const int lane = t & 31, w = t >> 5;
+    const int h = wk.h[u], p0 = wk.p0[u], nu = wk.nu;
+    UnitArrays& ua = tl.unit[u];
+    const uint32_t tm = tmem + ((uint32_t)(w * 32) << 16);
+    const float A = __ldg(rc.A + h), D = __ldg(rc.D + h);
+    const unsigned s_op = base + kOffS + u * kTileX;
+    const unsigned xs_hi = base + kOffXs, xs_lo = xs_hi + kTileX;
+    bool ok = true;
+    auto wait = [&](uint64_t* bar, unsigned parity) {
+        if (ok) ok = mbar_wait_suspend(bar, parity);
+        __syncwarp();               // the tensor-memory accesses are the whole warp's
+    };
+    auto write_state = [&]() {   // S in bf16, line n of the operand
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+            sts128(s_op + swz(t, c),
+                   make_uint4(pack_bf16(S[8 * c], S[8 * c + 1]), pack_bf16(S[8 * c + 2], S[8 * c + 3]),
+                              pack_bf16(S[8 * c + 4], S[8 * c + 5]),
+                              pack_bf16(S[8 * c + 6], S[8 * c + 7])));
+        fence_proxy_async();
+    };
+    if constexpr (!STATE) {
+        // M above the diagonal blocks stays zero
+        const uint32_t zero[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+        for (int k = 0; k < 64; k += 8) tc::st8(tm + col_m(u) + k, zero);
+        tc::wait_st();
+        write_state();
+    }
+    if (t < kPT) ua.bad[t] = kL;
+
+    const long long tok0 = (long long)wk.run.t0 + (long long)wk.c0 * kL;
+    const int left0 = wk.run.len - wk.c0 * kL;      // tokens from the segment's start
+    auto load_dt = [&](int c) {
+        return c < wk.nc && c * kL + t < left0
+                   ? __ldg(rc.dt + (tok0 + (long long)c * kL + t) * rc.dts + h) : 0.0f;
+    };
+    float dt = load_dt(0);
+    decay_all = 1.0f;
+
+    for (int c = 0; c < wk.nc; ++c) {
+        const int Lc = min(kL, left0 - c * kL);
+        const float dt_next = load_dt(c + 1);
+        // ---- running sums ----
+        float a = __fmul_rn(dt, A);
+        if (a < kStepFloor) a = kStepFloor;         // a NaN stays
+        if (t >= Lc) a = 0.0f;                      // dt is 0 there, A may be infinite
+        float r = a;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const float v = __shfl_up_sync(0xffffffffu, r, o);
+            if (lane >= o) r += v;
+        }
+        float q = __shfl_down_sync(0xffffffffu, a, 1);
+        if (lane == 31) q = 0.0f;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const float v = __shfl_down_sync(0xffffffffu, q, o);
+            if (lane + o < 32) q += v;
+        }
+        const float f = __fmul_rn(dt, expf(q));
+        ua.f[t] = f;
+        ua.r2[t] = __fmul_rn(r, kLog2e);
+        ua.dt[t] = dt;
+        if (lane == 31) ua.block[w] = r;
+        unit_sync(u);
+        float before = 0.0f, behind = 0.0f, total = 0.0f;
+        float between[3] = {0.0f, 0.0f, 0.0f};      // from block k's end to this block
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const float bs = ua.block[k];
+            total += bs;
+            if (k < w) before += bs;
+            if (k > w) behind += bs;
+#pragma unroll
+            for (int m = 0; m < 3; ++m)
+                if (m < k && k < w) between[m] += bs;
+        }
+        const float wj = __fmul_rn(f, expf(behind));
+        const float lam = expf(total);
+        decay_all = __fmul_rn(decay_all, lam);
+
+        // ---- w X in two parts ----
+        const int kx = c * nu + u, xslot = kx % kRingX;
+        const unsigned xrow = base + kOffX + xslot * kTileX;
+        wait(&tl.x_full[xslot], (kx / kRingX) & 1);
+        bool bad = false;
+        {
+            float2 acc = make_float2(0.0f, 0.0f);
+            const float2 w2 = make_float2(wj, wj), zero2 = make_float2(0.0f, 0.0f);
+            // the other unit's product has read the shared buffer
+            if (u == 0) {
+                if (c > 0) wait(&tl.ds_full[nu - 1], (c - 1) & 1);
+            } else {
+                wait(&tl.ds_full[0], c & 1);
+            }
+            const bool inside = t < Lc;
+#pragma unroll
+            for (int ch = 0; ch < 8; ++ch) {
+                uint4 xv = lds128(xrow + swz(t, ch));
+                if (!inside) xv = make_uint4(0, 0, 0, 0);
+                const uint32_t xw[4] = {xv.x, xv.y, xv.z, xv.w};
+                uint32_t hi[4], lo[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const float2 x2 = unpack_bf16(xw[k]);
+                    acc = fma2(x2, zero2, acc);
+                    float2 v = mul2(x2, w2);
+                    if (!inside) v = zero2;          // w may be NaN
+                    hi[k] = pack_bf16(v.x, v.y);
+                    const float2 hv = unpack_bf16(hi[k]);
+                    const float2 d = add2(v, make_float2(-hv.x, -hv.y));
+                    lo[k] = pack_bf16(d.x, d.y);
+                }
+                sts128(xs_hi + swz(t, ch), make_uint4(hi[0], hi[1], hi[2], hi[3]));
+                sts128(xs_lo + swz(t, ch), make_uint4(lo[0], lo[1], lo[2], lo[3]));
+                if (!inside && !STATE) sts128(xrow + swz(t, ch), make_uint4(0, 0, 0, 0));
+            }
+            bad = !(acc.x + acc.y == 0.0f);
+        }
+        if (bad) {
+            // rare: take the non-finite entries of this token out
+            for (int p = 0; p < kPT; ++p) {
+                const unsigned at = swz(t, p >> 3) + (p & 7) * 2;
+                unsigned short v;
+                asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(xrow + at) : "memory");
+                if ((v & 0x7f80u) == 0x7f80u) {
+                    atomicMin(&ua.bad[p], t);
+                    const unsigned short z = 0;
+                    asm volatile("st.shared.u16 [%0], %1;" :: "r"(xrow + at), "h"(z) : "memory");
+                    asm volatile("st.shared.u16 [%0], %1;" :: "r"(xs_hi + at), "h"(z) : "memory");
+                    asm volatile("st.shared.u16 [%0], %1;" :: "r"(xs_lo + at), "h"(z) : "memory");
+                }
+            }
+        }
+        __syncwarp();
+        fence_proxy_async();
+        mbar_arrive(&tl.xs_ready[u]);
+        if constexpr (STATE) mbar_arrive(&tl.x_empty[xslot]);
+        const bool any_bad = unit_any(u, bad);
+
+        // ---- M ----
+        if constexpr (!STATE) {
+            const float ri2 = __fmul_rn(r, kLog2e);
+            wait(&tl.g_full, c & 1);
+            tc::fence_after();
+            for (int k = 0; k <= w; ++k) {
+                const bool diag = k == w;
+                const float uk = diag ? 1.0f : expf(r + (k == 0 ? between[0] : k == 1 ? between[1]
+                                                                                 : between[2]));
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    const int j0 = 32 * k + 16 * half;
+                    float gv[16];
+                    tc::ld16(tm + kColG + j0, gv);
+                    float cf[16];
+                    if (!diag) {
+                        const float2 u2 = make_float2(uk, uk);
+#pragma unroll
+                        for (int m = 0; m < 16; m += 4) {
+                            const float4 fv = *reinterpret_cast<const float4*>(&ua.f[j0 + m]);
+                            const float2 c0 = mul2(make_float2(fv.x, fv.y), u2);
+                            const float2 c1 = mul2(make_float2(fv.z, fv.w), u2);
+                            cf[m] = c0.x; cf[m + 1] = c0.y; cf[m + 2] = c1.x; cf[m + 3] = c1.y;
+                        }
+                    } else {
+#pragma unroll
+                        for (int m = 0; m < 16; m += 4) {
+                            const float4 rv = *reinterpret_cast<const float4*>(&ua.r2[j0 + m]);
+                            const float4 dv = *reinterpret_cast<const float4*>(&ua.dt[j0 + m]);
+                            cf[m] = __fmul_rn(dv.x, ex2(__fsub_rn(ri2, rv.x)));
+                            cf[m + 1] = __fmul_rn(dv.y, ex2(__fsub_rn(ri2, rv.y)));
+                            cf[m + 2] = __fmul_rn(dv.z, ex2(__fsub_rn(ri2, rv.z)));
+                            cf[m + 3] = __fmul_rn(dv.w, ex2(__fsub_rn(ri2, rv.w)));
+                        }
+                    }
+                    tc::wait_ld(gv);
+                    uint32_t mw[8];
+#pragma unroll
+                    for (int m = 0; m < 16; m += 2) {
+                        float2 v = mul2(make_float2(gv[m], gv[m + 1]),
+                                        make_float2(cf[m], cf[m + 1]));
+                        if (diag) {                  // j > i: 0 whatever G holds there
+                            if (16 * half + m > lane) v.x = 0.0f;
+                            if (16 * half + m + 1 > lane) v.y = 0.0f;
+                        }
+                        mw[m / 2] = pack_bf16(v.x, v.y);
+                    }
+                    tc::st8(tm + col_m(u) + j0 / 2, mw);
+                }
+            }
+            tc::wait_st();
+            tc::fence_before();
+            mbar_arrive(&tl.g_free);
+        }
+
+        // ---- state ----
+        wait(&tl.ds_full[u], c & 1);
+        tc::fence_after();
+        {
+            const float2 l2 = make_float2(lam, lam);
+#pragma unroll
+            for (int k = 0; k < kPT; k += 16) {
+                float d[16];
+                tc::ld16(tm + col_y1(u) + k, d);
+                tc::wait_ld(d);
+#pragma unroll
+                for (int m = 0; m < 16; m += 2) {
+                    const float2 v = fma2(l2, make_float2(S[k + m], S[k + m + 1]),
+                                          make_float2(d[m], d[m + 1]));
+                    S[k + m] = v.x;
+                    S[k + m + 1] = v.y;
+                }
+            }
+        }
+        if (any_bad) {
+#pragma unroll
+            for (int p = 0; p < kPT; ++p)
+                if (ua.bad[p] < kL) S[p] = __int_as_float(0x7fffffff);
+        }
+        tc::fence_before();
+        if constexpr (!STATE) {
+            mbar_arrive(&tl.m_ready[u]);
+            if (c + 1 < wk.nc) write_state();       // Y2 of this chunk has read the old one
+
+            // ---- y ----
+            const float ei = expf(r + before);
+            wait(&tl.y_full[u], c & 1);
+            tc::fence_after();
+            const float2 e2 = make_float2(ei, ei), D2 = make_float2(D, D);
+#pragma unroll
+            for (int k = 0; k < kPT; k += 16) {
+                float y1[16], y2[16];
+                tc::ld16(tm + col_y1(u) + k, y1);
+                tc::ld16(tm + col_y2(u) + k, y2);
+                const uint4 xa = lds128(xrow + swz(t, k / 8)), xb = lds128(xrow + swz(t, k / 8 + 1));
+                tc::wait_ld(y1);
+                tc::after_wait(y2);
+                const uint32_t xw[8] = {xa.x, xa.y, xa.z, xa.w, xb.x, xb.y, xb.z, xb.w};
+                uint32_t yw[8];
+#pragma unroll
+                for (int m = 0; m < 16; m += 2) {
+                    float2 v = fma2(e2, make_float2(y2[m], y2[m + 1]), make_float2(y1[m], y1[m + 1]));
+                    v = fma2(D2, unpack_bf16(xw[m / 2]), v);
+                    if (any_bad) {
+                        if (ua.bad[k + m] <= t) v.x = __int_as_float(0x7fffffff);
+                        if (ua.bad[k + m + 1] <= t) v.y = __int_as_float(0x7fffffff);
+                    }
+                    yw[m / 2] = pack_bf16(v.x, v.y);
+                }
+                sts128(xrow + swz(t, k / 8), make_uint4(yw[0], yw[1], yw[2], yw[3]));
+                sts128(xrow + swz(t, k / 8 + 1), make_uint4(yw[4], yw[5], yw[6], yw[7]));
+            }
+            tc::fence_before();
+            unit_sync(u);
+            // rows of 128 bytes by 8 lanes each
+            if (ok) {
+                const int ch = t & 7;
+                __nv_bfloat16* yp = reinterpret_cast<__nv_bfloat16*>(rc.y)
+                                    + (tok0 + (long long)c * kL) * rc.ys + (long long)h * pv.P + p0
+                                    + ch * 8;
+                if (p0 + ch * 8 < pv.P) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const int row = i * 16 + (t >> 3);
+                        if (row < Lc) {
+                            const uint4 v = lds128(xrow + swz(row, ch));
+                            __stcs(reinterpret_cast<uint4*>(yp + (long long)row * rc.ys), v);
+                        }
+                    }
+                }
+            }
+            fence_proxy_async();
+            mbar_arrive(&tl.x_empty[xslot]);
+        } else {
+            unit_sync(u);                           // `bad` is read by all before it is reset
+        }
+        if (any_bad && t < kPT) ua.bad[t] = kL;
+        dt = dt_next;
+    }
+    return ok;
+}
+
+template <bool STATE>
+__global__ void __launch_bounds__(kCThreadsTotal, 1)
+chunk_kernel(const __grid_constant__ PoolView pv, const __grid_constant__ RaggedCall rc,
+             const __grid_constant__ ChunkMaps maps, int fmt)
+{
+    extern __shared__ unsigned char smem_raw[];
+    const unsigned raw = saddr(smem_raw);
+    unsigned char* sm = smem_raw + ((1024 - (raw & 1023)) & 1023);
+    const unsigned base = saddr(sm);
+    Tail& tl = *reinterpret_cast<Tail*>(sm + kOffTail);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+    // ---- the block's work: pairs of units fastest, then requests, then segments
+    const int tiles = (pv.P + kPT - 1) / kPT;
+    const int per_group = pv.hpg * tiles, pairs_group = (per_group + 1) / 2;
+    const int pairs = pairs_group * pv.G;
+    Work wk;
+    {
+        const int pr = blockIdx.x % pairs;
+        const int rest = blockIdx.x / pairs;
+        wk.b = rest % rc.batch;
+        wk.seg = rest / rc.batch;
+        wk.g = pr / pairs_group;
+        const int u0 = (pr - wk.g * pairs_group) * 2;
+        wk.nu = min(2, per_group - u0);
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            const int uu = min(u0 + u, per_group - 1);
+            wk.h[u] = wk.g * pv.hpg + uu / tiles;
+            wk.p0[u] = uu % tiles * kPT;
+        }
+    }
+    wk.run = ragged_run(pv, rc, wk.b, false);       // the token kernel reports
+    if (!wk.run.ok || wk.run.len < rc.chunk_min) return;
+    const int chunks = (wk.run.len + kL - 1) / kL;
+    wk.nseg = rc.nseg > 1 ? (chunks + rc.seg_chunks - 1) / rc.seg_chunks : 1;
+    wk.c0 = rc.nseg > 1 ? wk.seg * rc.seg_chunks : 0;
+    wk.nc = rc.nseg > 1 ? min(rc.seg_chunks, chunks - wk.c0) : chunks;
+    if (wk.seg >= wk.nseg || (STATE && wk.seg + 1 >= wk.nseg)) return;
+    const int nu = wk.nu, nc = wk.nc;
+
+    // ---- set-up ----
+    if (tid == 0) {
+        for (int i = 0; i < kRingCB; ++i) {
+            mbar_init(&tl.cb_full[i], 1);
+            mbar_init(&tl.cb_empty[i], 1);
+        }
+        for (int i = 0; i < kRingX; ++i) {
+            mbar_init(&tl.x_full[i], 1);
+            mbar_init(&tl.x_empty[i], kWg);
+        }
+        for (int u = 0; u < 2; ++u) {
+            mbar_init(&tl.xs_ready[u], kWg);
+            mbar_init(&tl.ds_full[u], 1);
+            mbar_init(&tl.m_ready[u], kWg);
+            mbar_init(&tl.y_full[u], 1);
+        }
+        mbar_init(&tl.g_full, 1);
+        mbar_init(&tl.g_free, kWg * nu);
+        mbar_init(&tl.drained, 1);
+        fence_proxy_async();
+    }
+    for (int i = tid; i < pv.H; i += kCThreadsTotal)
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+            if (pv.perm[i] == wk.h[u]) tl.pos[u] = i;
+    if (warp == 9) tc::alloc(&tl.tmem, kTmemCols);
+    tc::fence_before();
+    __syncthreads();
+    tc::fence_after();
+    const uint32_t tmem = tl.tmem;
+    const int halves = pv.N > 64 ? 2 : 1;           // 64-column halves of C and B
+    bool ok = true;
+
+    if (warp < 8) {
+        const int u = warp >> 2, t = tid & (kWg - 1);
+        const bool mine = u < nu;
+        const int h = wk.h[u], p0 = wk.p0[u];
+        float S[kPT];
+        float decay_all = 1.0f;
+        // staging of the states at the ends: w X's buffer and the bf16 states'
+        float* stage = reinterpret_cast<float*>(sm + (u == 0 ? kOffXs : kOffS));
+        const long long unit_state = ((long long)h * pv.P + p0) * pv.N;
+        const long long seg_state = ((long long)wk.b * rc.nseg + wk.seg) * pv.H * pv.P * pv.N;
+#pragma unroll
+        for (int p = 0; p < kPT; ++p) S[p] = 0.0f;
+        if (mine && !STATE) {
+            if (wk.nseg > 1) {
+                const float* src = rc.ws_state + seg_state + unit_state + t;
+#pragma unroll
+                for (int p = 0; p < kPT; ++p)
+                    if (t < pv.N && p0 + p < pv.P) S[p] = src[p * pv.N];
+            } else if (!wk.run.fresh) {
+                unit_io_any(fmt, true, pv, wk.run.slot, rc.layer, tl.pos[u], p0, stage, t);
+                unit_sync(u);
+#pragma unroll
+                for (int p = 0; p < kPT; ++p)
+                    if (t < pv.N) S[p] = stage[p * pv.N + t];
+            }
+        }
+        units_sync();       // the staging is read before the loops write there
+        if (mine) ok = unit_loop<STATE>(pv, rc, wk, base, tl, tmem, u, t, S, decay_all);
+        units_sync();       // the loops are done with the staging
+        if (mine && ok) {
+            if constexpr (STATE) {
+                float* dst = rc.ws_state + seg_state + unit_state + t;
+#pragma unroll
+                for (int p = 0; p < kPT; ++p)
+                    if (t < pv.N && p0 + p < pv.P) dst[p * pv.N] = S[p];
+                if (t == 0 && p0 == 0)
+                    rc.ws_decay[((long long)wk.b * rc.nseg + wk.seg) * pv.H + h] = decay_all;
+            } else if (wk.seg + 1 == wk.nseg) {
+#pragma unroll
+                for (int p = 0; p < kPT; ++p)
+                    if (t < pv.N) stage[p * pv.N + t] = S[p];
+                unit_sync(u);
+                unit_io_any(fmt, false, pv, wk.run.slot, rc.layer, tl.pos[u], p0, stage, t);
+            }
+        }
+    } else if (warp == 8) {
+        // ---- tensor copies ----
+        if (lane == 0) {
+            const int tok0 = wk.run.t0 + wk.c0 * kL;
+            int k = 0, kx = 0;
+            for (int c = 0; c < nc && ok; ++c) {
+                const int tok = tok0 + c * kL;
+                for (int which = STATE ? 1 : 0; which < 2 && ok; ++which, ++k) {   // C, then B
+                    const int s = k % kRingCB;
+                    if (k >= kRingCB) ok = mbar_wait_suspend(&tl.cb_empty[s], (k / kRingCB - 1) & 1);
+                    if (!ok) break;
+                    mbar_arrive_tx(&tl.cb_full[s], (unsigned)(halves * kTileX));
+                    for (int hf = 0; hf < halves; ++hf)
+                        tc::tma_load3(sm + s * kTileCB + hf * kTileX, which ? &maps.B : &maps.C,
+                                      hf * 64, wk.g, tok, &tl.cb_full[s]);
+                }
+                for (int u = 0; u < nu && ok; ++u, ++kx) {
+                    const int s = kx % kRingX;
+                    if (kx >= kRingX) ok = mbar_wait_suspend(&tl.x_empty[s], (kx / kRingX - 1) & 1);
+                    if (!ok) break;
+                    mbar_arrive_tx(&tl.x_full[s], kTileX);
+                    tc::tma_load3(sm + kOffX + s * kTileX, &maps.x, wk.p0[u], wk.h[u], tok,
+                                  &tl.x_full[s]);
+                }
+            }
+            // no copy is in flight when the block ends, whatever happened
+            for (int i = max(0, k - kRingCB); i < k; ++i)
+                mbar_wait_suspend(&tl.cb_full[i % kRingCB], (i / kRingCB) & 1);
+            for (int i = max(0, kx - kRingX); i < kx; ++i)
+                mbar_wait_suspend(&tl.x_full[i % kRingX], (i / kRingX) & 1);
+        }
+        __syncwarp();
+    } else {
+        // ---- products ----
+        // Events in whatever order their operands become ready; the sums do
+        // not depend on it.  g, xs, m: chunks whose G, whose Y2 and dS, and
+        // whose Y1 have been issued.
+        constexpr uint32_t kShapeG = tc::shape(128, 128, false, false);
+        constexpr uint32_t kShapeY = tc::shape(128, 64, false, true);
+        constexpr uint32_t kShapeS = tc::shape(128, 64, true, true);
+        const int nk = halves * 4;                  // steps of 16 over d_state
+        int g = 0, xs[2] = {0, nu > 1 ? 0 : nc}, m[2] = {STATE ? nc : 0, STATE || nu == 1 ? nc : 0};
+        long long t0 = clock64();
+        const int last_len = wk.run.len - (wk.c0 + nc - 1) * kL;
+        auto slot_c = [&](int c) { return (2 * c) % kRingCB; };
+        auto slot_b = [&](int c) { return (STATE ? c : 2 * c + 1) % kRingCB; };
+        auto par_c = [&](int c) { return (unsigned)((2 * c / kRingCB) & 1); };
+        auto par_b = [&](int c) { return (unsigned)(((STATE ? c : 2 * c + 1) / kRingCB) & 1); };
+        while (g < nc || xs[0] < nc || xs[1] < nc || m[0] < nc || m[1] < nc) {
+            int ev = -1;
+            if (lane == 0) {
+                for (int u = 0; u < 2 && ev < 0; ++u)
+                    if (m[u] < xs[u] && m[u] < nc && mbar_try(&tl.m_ready[u], m[u] & 1)) ev = u;
+                for (int u = 0; u < 2 && ev < 0; ++u)
+                    if (xs[u] < g && xs[u] < nc && mbar_try(&tl.xs_ready[u], xs[u] & 1)) ev = 2 + u;
+                if (ev < 0 && g < nc && (STATE || g == 0 || mbar_try(&tl.g_free, (g - 1) & 1))
+                    && (STATE || mbar_try(&tl.cb_full[slot_c(g)], par_c(g)))
+                    && mbar_try(&tl.cb_full[slot_b(g)], par_b(g)))
+                    ev = 4;
+            }
+            ev = __shfl_sync(0xffffffffu, ev, 0);
+            if (ev < 0) {
+                const bool late = clock64() - t0 > kWaitLimit;
+                if (__shfl_sync(0xffffffffu, (int)late, 0)) {
+                    ok = false;
+                    break;
+                }
+                __nanosleep(20);
+                continue;
+            }
+            t0 = clock64();
+            tc::fence_after();
+            if (ev == 4) {
+                const unsigned sb = base + slot_b(g) * kTileCB;
+                if (g == nc - 1 && last_len < kL) {
+                    // lines of B past the run's end
+                    mbar_try(&tl.cb_full[slot_b(g)], par_b(g));
+                    for (int i = lane; i < (kL - last_len) * 8; i += 32)
+                        for (int hf = 0; hf < halves; ++hf)
+                            sts128(sb + hf * kTileX + last_len * 128 + i * 16,
+                                   make_uint4(0, 0, 0, 0));
+                    fence_proxy_async();
+                    __syncwarp();
+                }
+                if (!STATE && lane == 0) {
+                    const unsigned sc = base + slot_c(g) * kTileCB;
+                    for (int k = 0; k < nk; ++k) {
+                        const unsigned o = (k >> 2) * kTileX + (k & 3) * 32;
+                        tc::mma(tmem + kColG, tc::operand(sc + o), tc::operand(sb + o), kShapeG,
+                                k > 0);
+                    }
+                    tc::commit(&tl.g_full);
+                }
+                ++g;
+            } else if (ev >= 2) {
+                const int u = ev - 2, c = xs[u];
+                const unsigned sb = base + slot_b(c) * kTileCB;
+                const bool both = xs[u ^ 1] > c;    // the chunk's C and B are done with
+                if (lane == 0) {
+                    if (!STATE) {
+                        const unsigned sc = base + slot_c(c) * kTileCB;
+                        const unsigned so = base + kOffS + u * kTileX;
+                        for (int k = 0; k < nk; ++k)
+                            tc::mma(tmem + col_y2(u),
+                                    tc::operand(sc + (k >> 2) * kTileX + (k & 3) * 32),
+                                    tc::operand(so + k * 2048), kShapeY, k > 0);
+                    }
+                    for (int part = 0; part < 2; ++part)
+                        for (int k = 0; k < kL / 16; ++k)
+                            tc::mma(tmem + col_y1(u), tc::operand(sb + k * 2048, kTileX),
+                                    tc::operand(base + kOffXs + part * kTileX + k * 2048), kShapeS,
+                                    part + k > 0);
+                    tc::commit(&tl.ds_full[u]);
+                    if (both) {
+                        if (!STATE) tc::commit(&tl.cb_empty[slot_c(c)]);
+                        tc::commit(&tl.cb_empty[slot_b(c)]);
+                    }
+                }
+                ++xs[u];
+            } else {
+                const int u = ev, c = m[u];
+                if (lane == 0) {
+                    const unsigned sx = base + kOffX + ((c * nu + u) % kRingX) * kTileX;
+                    for (int k = 0; k < kL / 16; ++k)
+                        tc::mma_ta(tmem + col_y1(u), tmem + col_m(u) + k * 8,
+                                   tc::operand(sx + k * 2048), kShapeY, k > 0);
+                    tc::commit(&tl.y_full[u]);
+                }
+                ++m[u];
+            }
+        }
+        // the products are complete before the memory they use goes away
+        if (lane == 0) {
+            tc::commit(&tl.drained);
+            mbar_wait_suspend(&tl.drained, 0);
+        }
+        __syncwarp();
+    }
+    if (!ok) atomicOr(reinterpret_cast<unsigned*>(pv.pool), SSQ_DEVERR_TIMEOUT);
+    tc::fence_before();
+    __syncthreads();
+    tc::fence_after();
+    if (warp == 9) tc::dealloc(tmem, kTmemCols);
+}
+
+// ---------------------------------------------------------------------------
+// Segments' starting states: S_0 from the pool (or zero), S_{k+1} = decay_k
+// S_k + state_k; S_k replaces state_k in the workspace.  The lanes of a row
+// hold E entries each, as in the pool.
+// ---------------------------------------------------------------------------
+template <int FMT, int N>
+__global__ void __launch_bounds__(kThreads)
+chunk_join(const __grid_constant__ PoolView pv, const __grid_constant__ RaggedCall rc)
+{
+    constexpr int E = Shape<N>::E, LPR = Shape<N>::LPR;
+    constexpr int kRows = kThreads / LPR;
+    const int tiles = (pv.P + kRows - 1) / kRows;
+    const int per = tiles * pv.H;
+    const int b = blockIdx.x / per, unit = blockIdx.x - b * per;
+    const int pos = unit / tiles, h = pv.perm[pos];
+    const Run run = ragged_run(pv, rc, b, false);
+    if (!run.ok || run.len < rc.chunk_min) return;
+    const int nseg = ((run.len + kL - 1) / kL + rc.seg_chunks - 1) / rc.seg_chunks;
+    if (nseg < 2) return;
+    const int j = threadIdx.x % LPR, p = unit % tiles * kRows + threadIdx.x / LPR;
+    const bool active = p < pv.P;
+    float s[E];
+    if (run.fresh) {
+#pragma unroll
+        for (int n = 0; n < E; ++n) s[n] = 0.0f;
+    } else {
+        row_load<FMT, N>(place_head<FMT>(pv, run.slot, rc.layer, pos), p, j, active, s);
+    }
+    if (!active) return;
+    const long long seg_floats = (long long)pv.H * pv.P * N;
+    float* at = rc.ws_state + (long long)b * rc.nseg * seg_floats
+                + ((long long)h * pv.P + p) * N + j * E;
+    const float* dec = rc.ws_decay + (long long)b * rc.nseg * pv.H + h;
+    for (int k = 0; k < nseg; ++k, at += seg_floats, dec += pv.H) {
+        const float l = k + 1 < nseg ? *dec : 0.0f;
+#pragma unroll
+        for (int n = 0; n < E; n += 4) {
+            float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            if (k + 1 < nseg) v = *reinterpret_cast<const float4*>(at + n);
+            *reinterpret_cast<float4*>(at + n) = make_float4(s[n], s[n + 1], s[n + 2], s[n + 3]);
+            s[n] = __fmaf_rn(l, s[n], v.x);
+            s[n + 1] = __fmaf_rn(l, s[n + 1], v.y);
+            s[n + 2] = __fmaf_rn(l, s[n + 2], v.z);
+            s[n + 3] = __fmaf_rn(l, s[n + 3], v.w);
+        }
+    }
+}
+
+template <int FMT, int N>
+cudaError_t join_n(const PoolView& pv, const RaggedCall& rc, cudaStream_t st)
+{
+    constexpr int kRows = kThreads / Shape<N>::LPR;
+    const unsigned grid = (unsigned)((pv.P + kRows - 1) / kRows * pv.H * rc.batch);
+    chunk_join<FMT, N><<<grid, kThreads, 0, st>>>(pv, rc);
+    return cudaGetLastError();
+}
+template <int FMT>
+cudaError_t join_fmt(const PoolView& pv, const RaggedCall& rc, cudaStream_t st)
+{
+    switch (pv.N) {
+    case 16: return join_n<FMT, 16>(pv, rc, st);
+    case 32: return join_n<FMT, 32>(pv, rc, st);
+    case 64: return join_n<FMT, 64>(pv, rc, st);
+    default: return join_n<FMT, 128>(pv, rc, st);
+    }
+}
+cudaError_t join(const PoolView& pv, const RaggedCall& rc, int fmt, cudaStream_t st)
+{
+    switch (fmt) {
+    case SSQ_F32: return join_fmt<SSQ_F32>(pv, rc, st);
+    case SSQ_BF16: return join_fmt<SSQ_BF16>(pv, rc, st);
+    case SSQ_I8_SYM: return join_fmt<SSQ_I8_SYM>(pv, rc, st);
+    case SSQ_I8_ASYM: return join_fmt<SSQ_I8_ASYM>(pv, rc, st);
+    case SSQ_I4_SYM: return join_fmt<SSQ_I4_SYM>(pv, rc, st);
+    default: return join_fmt<SSQ_I4_ASYM>(pv, rc, st);
+    }
+}
+
+// The driver's tensor-map encoder, looked up once through the runtime.
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder()
+{
+    static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult q = cudaDriverEntryPointSymbolNotFound;
+        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) !=
+                cudaSuccess || q != cudaDriverEntryPointSuccess)
+            p = nullptr;
+        return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+    }();
+    return fn;
+}
+
+// [token][group or head][64-column piece] boxes of 128 tokens.
+cudaError_t make_map(CUtensorMap* map, const void* base, int inner, int mid, long long total,
+                     long long stride)
+{
+    PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
+    if (!enc) return cudaErrorNotSupported;
+    cuuint64_t dims[3] = {(cuuint64_t)inner, (cuuint64_t)mid, (cuuint64_t)total};
+    cuuint64_t strides[2] = {(cuuint64_t)inner * 2, (cuuint64_t)stride * 2};
+    cuuint32_t box[3] = {64, 1, kL};
+    cuuint32_t estr[3] = {1, 1, 1};
+    const CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims,
+                           strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                           CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+int chunk_pairs(int H, int P, int G)
+{
+    const int per_group = H / G * ((P + kPT - 1) / kPT);
+    return (per_group + 1) / 2 * G;
+}
+
+template <bool STATE>
+cudaError_t launch_pass(const PoolView& pv, const RaggedCall& rc, const ChunkMaps& maps, int fmt,
+                        cudaStream_t st)
+{
+    cudaError_t e = cudaFuncSetAttribute(chunk_kernel<STATE>,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+    if (e != cudaSuccess) return e;
+    const long long blocks = (long long)chunk_pairs(pv.H, pv.P, pv.G) * rc.batch * rc.nseg;
+    if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+    chunk_kernel<STATE><<<(unsigned)blocks, kCThreadsTotal, kSmemBytes, st>>>(pv, rc, maps, fmt);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+void chunk_plan(int H, int P, int N, int G, int batch, int max_len, int* nseg, int* seg_chunks)
+{
+    *nseg = 1;
+    *seg_chunks = 1;
+    if (N > 128 || batch < 1) return;
+    const int chunks = (int)(((long long)max_len + kL - 1) / kL);
+    const long long blocks = (long long)chunk_pairs(H, P, G) * batch;
+    const long long fit = kSMs / blocks;
+    long long n = chunks / 4 < fit ? chunks / 4 : fit;
+    if (n < 2) return;
+    *seg_chunks = (int)((chunks + n - 1) / n);
+    *nseg = (chunks + *seg_chunks - 1) / *seg_chunks;
+}
+
+cudaError_t launch_ragged_chunks(const PoolView& pv, const RaggedCall& rc, int fmt,
+                                 cudaStream_t st)
+{
+    ChunkMaps maps;
+    std::memset(&maps, 0, sizeof(maps));
+    cudaError_t e = make_map(&maps.x, rc.x, pv.P, pv.H, rc.total, rc.xs);
+    if (e == cudaSuccess) e = make_map(&maps.B, rc.B, pv.N, pv.G, rc.total, rc.Bs);
+    if (e == cudaSuccess) e = make_map(&maps.C, rc.C, pv.N, pv.G, rc.total, rc.Cs);
+    if (e == cudaSuccess && rc.nseg > 1) {
+        e = launch_pass<true>(pv, rc, maps, fmt, st);
+        if (e == cudaSuccess) e = join(pv, rc, fmt, st);
+    }
+    if (e == cudaSuccess) e = launch_pass<false>(pv, rc, maps, fmt, st);
+    return e;
+}
+
+}  // namespace ssq

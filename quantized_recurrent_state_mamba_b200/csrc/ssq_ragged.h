@@ -12,7 +12,6 @@ struct RaggedCall {
     const uint8_t* fresh;      // [batch] or null
     int batch, layer, max_len;
     int chunk_min;             // runs of at least this many tokens go through chunks
-    int chunked;               // the chunk kernel runs beside the token kernel
     long long total;
     int type;                  // ssq_dtype
     const void *x, *B, *C;
@@ -56,5 +55,9 @@ __device__ __forceinline__ Run ragged_run(const PoolView& pv, const RaggedCall& 
 // (ssq_chunk.cu).
 cudaError_t launch_ragged_tokens(const PoolView& pv, const RaggedCall& rc, int fmt,
                                  cudaStream_t st);
+cudaError_t launch_ragged_chunks(const PoolView& pv, const RaggedCall& rc, int fmt,
+                                 cudaStream_t st);
+// Segments that the longest run is cut into, and their length in chunks.
+void chunk_plan(int H, int P, int N, int G, int batch, int max_len, int* nseg, int* seg_chunks);
 
 }  // namespace ssq

@@ -11,6 +11,9 @@ using namespace ssq::host;
 
 namespace {
 
+// Runs of at least this many tokens go through chunks.
+constexpr int kChunkMin = 32;
+
 size_t elem_bytes(ssq_dtype t) { return t == SSQ_T_F32 ? 4 : 2; }
 
 ssq_status check_type(ssq_dtype t)
@@ -55,6 +58,26 @@ ssq_status check_reorder(int n_layers, int n_slots, const int32_t* slot_idx, int
     return batch > 0 ? need(parent, "parent", 4) : SSQ_OK;
 }
 
+// The workspace of a call whose runs are cut into nseg segments: a state and
+// a decay per request, segment and head.
+size_t segment_state_bytes(const ssq_config* cfg, int batch, int nseg)
+{
+    return (size_t)batch * nseg * cfg->nheads * cfg->headdim * cfg->d_state * 4;
+}
+size_t segment_decay_bytes(const ssq_config* cfg, int batch, int nseg)
+{
+    return (size_t)batch * nseg * cfg->nheads * 4;
+}
+
+// Whether the chunk kernel takes the call: bf16, whole 16-byte pieces.
+bool chunks_fit(const ssq_config* cfg, const ssq_tokens* t)
+{
+    return t->type == SSQ_T_BF16 && cfg->headdim % 8 == 0 && cfg->d_state <= 128 && t->total > 0
+           && t->x_stride % 8 == 0 && t->B_stride % 8 == 0 && t->C_stride % 8 == 0
+           && t->y_stride % 8 == 0 && aligned(t->x, 16) && aligned(t->B, 16)
+           && aligned(t->C, 16) && aligned(t->y, 16);
+}
+
 ssq_status run_reorder(const ssq::ReorderCall& rc, cudaStream_t stream)
 {
     if (rc.batch == 0) return SSQ_OK;
@@ -75,7 +98,11 @@ ssq_status ssq_prefill_ragged_workspace(const ssq_config* cfg, int batch, int ma
     if (batch < 0) return fail(SSQ_ERR_INVALID_ARG, "batch %d < 0", batch);
     if (max_len < 0) return fail(SSQ_ERR_INVALID_ARG, "max_len %d < 0", max_len);
     if (!bytes) return fail(SSQ_ERR_INVALID_ARG, "bytes is NULL");
-    *bytes = 0;
+    int nseg = 1, seg_chunks = 1;
+    ssq::chunk_plan(cfg->nheads, cfg->headdim, cfg->d_state, cfg->ngroups, batch, max_len, &nseg,
+                    &seg_chunks);
+    *bytes = nseg > 1 ? segment_state_bytes(cfg, batch, nseg) + segment_decay_bytes(cfg, batch, nseg)
+                      : 0;
     return SSQ_OK;
 }
 
@@ -144,7 +171,18 @@ ssq_status ssq_prefill_ragged(const ssq_config* cfg, void* pool, const int32_t* 
     rc.Cs = tok->C_stride;
     rc.dts = tok->dt_stride;
     rc.ys = tok->y_stride;
-    const cudaError_t e = ssq::launch_ragged_tokens(pv, rc, (int)cfg->fmt, stream);
+    const bool chunked = max_len >= kChunkMin && chunks_fit(cfg, tok);
+    if (chunked) {
+        rc.chunk_min = kChunkMin;
+        ssq::chunk_plan(cfg->nheads, cfg->headdim, cfg->d_state, cfg->ngroups, batch, max_len,
+                        &rc.nseg, &rc.seg_chunks);
+        if (rc.nseg > 1) {
+            rc.ws_state = static_cast<float*>(workspace);
+            rc.ws_decay = rc.ws_state + segment_state_bytes(cfg, batch, rc.nseg) / 4;
+        }
+    }
+    cudaError_t e = ssq::launch_ragged_tokens(pv, rc, (int)cfg->fmt, stream);
+    if (e == cudaSuccess && chunked) e = ssq::launch_ragged_chunks(pv, rc, (int)cfg->fmt, stream);
     if (e != cudaSuccess) return cuda_fail(e, "prefill_ragged launch");
     return SSQ_OK;
 }
