@@ -10,13 +10,13 @@
 //
 // A block owns two units, a unit being 64 rows (p) of one head, both in one
 // group of B and C, and walks their chunks with the states in registers.
-// Warps 0-3 and 4-7 do the element work of one unit each, warp 8 issues the
-// tensor copies, warp 9 the products:
+// Warps 0-7 and 8-15 do the element work of one unit each, warp 16 issues the
+// tensor copies, warps 17 to 19 the products (G; those of unit 0; of unit 1):
 //   G       [128 i x 128 j]  C and B from shared memory; TMEM
 //   Y2      [128 i x  64 p]  C times the state rounded to bf16; TMEM
-//   dS      [128 n x  64 p]  B^T times w X, the latter as the sum of two bf16
-//                            parts, so that the state sees its inputs to 16
-//                            bits and more; TMEM
+//   dS      [128 n x  64 p]  B^T times w X, the latter as the sum of two or
+//                            three bf16 parts, so that the state sees its
+//                            inputs to 16 or 24 bits; TMEM
 //   Y1      [128 i x  64 p]  M (bf16, written to TMEM) times X; the columns of
 //                            dS, which has been read by then
 // The running sums are kept per block of 32 tokens: with r_i the sum from the
@@ -49,36 +49,37 @@ namespace {
 
 constexpr int kL = 128;                 // tokens of a chunk
 constexpr int kPT = 64;                 // rows of a unit
-constexpr int kWg = 128;                // threads that work on a unit
-constexpr int kCThreadsTotal = 2 * kWg + 64;
+constexpr int kWg = 256;                // threads that work on a unit
+constexpr int kCThreadsTotal = 2 * kWg + 128;
+constexpr int kElemWarps = 2 * kWg / 32;
 constexpr float kLog2e = 1.4426950408889634f;
 // exp(-1000) is 0 in fp32: sums of clamped steps stay finite for A = -inf
 constexpr float kStepFloor = -1000.0f;
 
-// Shared memory, from a 1024-byte aligned base.
+// Shared memory, from its 1024-byte aligned start (the swizzle's period).
 constexpr int kTileCB = kL * 256;       // C or B: two halves of [128][64] bf16
 constexpr int kTileX = kL * 128;        // [128][64] bf16
 constexpr int kRingCB = 3, kRingX = 3;
 constexpr int kOffX = kRingCB * kTileCB;
-constexpr int kOffXs = kOffX + kRingX * kTileX;      // two bf16 parts of w X
-constexpr int kOffS = kOffXs + 2 * kTileX;           // states in bf16, one per unit
+constexpr int kOffXs = kOffX + kRingX * kTileX;      // up to three bf16 parts of w X
+constexpr int kOffS = kOffXs + 3 * kTileX;           // states in bf16, one per unit
 constexpr int kOffTail = kOffS + 2 * kTileX;
 
 struct UnitArrays {
     float f[kL];        // dt_j exp(q_j)
-    float r2[kL];       // r_j log2(e)
-    float dt[kL];
+    float r2[kL];       // r_j log2(e) - log2(dt_j)
     float block[4];     // sums of the four blocks
     int bad[kPT];       // first token of the chunk with a non-finite x in row p
+    int any_bad, pad[3];
 };
 struct Tail {
     UnitArrays unit[2];
     uint64_t cb_full[kRingCB], cb_empty[kRingCB], x_full[kRingX], x_empty[kRingX];
-    uint64_t xs_ready[2], ds_full[2], m_ready[2], y_full[2], g_full, g_free, drained;
+    uint64_t xs_ready[2], ds_full[2], m_ready[2], y_full[2], g_full, g_free, b_ready, drained[3];
     uint32_t tmem;
     int pos[2];         // region positions of the units' heads
 };
-constexpr int kSmemBytes = kOffTail + (int)sizeof(Tail) + 1024;
+constexpr int kSmemBytes = kOffTail + (int)sizeof(Tail);
 static_assert(kSmemBytes <= 227 * 1024, "shared memory");
 
 // TMEM columns.
@@ -91,14 +92,6 @@ __host__ __device__ constexpr uint32_t col_y2(int u) { return col_m(u) + 128; }
 __device__ __forceinline__ void unit_sync(int u)
 {
     asm volatile("bar.sync %0, %1;" :: "r"(1 + u), "n"(kWg) : "memory");
-}
-__device__ __forceinline__ bool unit_any(int u, bool v)
-{
-    unsigned r;
-    asm volatile("{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n"
-                 " barrier.red.or.pred q, %2, %3, p;\n selp.u32 %0, 1, 0, q;\n}\n"
-                 : "=r"(r) : "r"((unsigned)v), "r"(1 + u), "n"(kWg) : "memory");
-    return r != 0;
 }
 __device__ __forceinline__ void units_sync()
 {
@@ -207,7 +200,7 @@ __device__ __noinline__ void unit_io_any(int fmt, bool load, const PoolView& pv,
 }
 
 struct ChunkMaps {
-    CUtensorMap x, B, C;
+    CUtensorMap x, B, C, y;
 };
 
 // What a block works on.
@@ -220,13 +213,58 @@ struct Work {
 };
 
 // ---------------------------------------------------------------------------
-// Element work of unit u: 128 threads; thread t is token t of the chunk for
-// x, M and y, and entry n = t of the state.
+// Element work of unit u: 256 threads.  Thread (t, hf) is token t of the chunk
+// for x, M and y, and entry n = t of the state, each for half of the columns:
+// rows p in [32 hf, 32 hf + 32), and of every 32 columns of M the 16 from 16 hf.
 // ---------------------------------------------------------------------------
+constexpr int kPH = kPT / 2;
+
+// Token t's part of w X: NP bf16 parts (hi, the rest, the rest of that) to
+// shared memory.  With FULL the chunk has 128 tokens; otherwise tokens that
+// are not `inside` become zero.  Returns a sum that is 0 unless an x is not
+// finite.
+template <int NP, bool FULL, bool ZERO_X>
+__device__ __forceinline__ float weigh_x(unsigned xrow, unsigned xs, int t, int hf, float wj,
+                                         bool inside)
+{
+    const float2 w2 = make_float2(wj, wj), zero2 = make_float2(0.0f, 0.0f);
+    float2 acc = zero2;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const unsigned at = swz(t, 4 * hf + i);
+        uint4 xv = lds128(xrow + at);
+        if (!FULL && !inside) xv = make_uint4(0, 0, 0, 0);
+        const uint32_t xw[4] = {xv.x, xv.y, xv.z, xv.w};
+        uint32_t part[NP][4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const float2 x2 = unpack_bf16(xw[k]);
+            acc = fma2(x2, zero2, acc);
+            float2 v = mul2(x2, w2);
+            if (!FULL && !inside) v = zero2;         // w may be NaN
+#pragma unroll
+            for (int q = 0; q < NP; ++q) {
+                part[q][k] = pack_bf16(v.x, v.y);
+                if (q + 1 < NP) {
+                    const float2 h = unpack_bf16(part[q][k]);
+                    v = fma2(h, make_float2(-1.0f, -1.0f), v);   // exact
+                }
+            }
+        }
+#pragma unroll
+        for (int q = 0; q < NP; ++q)
+            sts128(xs + q * kTileX + at,
+                   make_uint4(part[q][0], part[q][1], part[q][2], part[q][3]));
+        if (!FULL && ZERO_X && !inside) sts128(xrow + at, make_uint4(0, 0, 0, 0));
+    }
+    return acc.x + acc.y;
+}
+
 template <bool STATE>
-__device__ __forceinline__ bool unit_loop(const PoolView& pv, const RaggedCall& rc, const Work& wk,
-                                          unsigned base, Tail& tl, uint32_t tmem, int u, int t,
-                                          float (&S)[kPT], float& decay_all)
+__device__ __forceinline__ bool unit_loop(const PoolView& pv, const RaggedCall& rc,
+                                          const CUtensorMap* ymap, const Work& wk,
+                                          unsigned char* sm, unsigned base, Tail& tl, uint32_t tmem, int u, int t,
+                                          int hf, int parts, float (&S)[kPH], float& decay_all)
 {
     const int lane = t & 31, w = t >> 5;
     const int h = wk.h[u], p0 = wk.p0[u], nu = wk.nu;
@@ -234,7 +272,7 @@ __device__ __forceinline__ bool unit_loop(const PoolView& pv, const RaggedCall& 
     const uint32_t tm = tmem + ((uint32_t)(w * 32) << 16);
     const float A = __ldg(rc.A + h), D = __ldg(rc.D + h);
     const unsigned s_op = base + kOffS + u * kTileX;
-    const unsigned xs_hi = base + kOffXs, xs_lo = xs_hi + kTileX;
+    const unsigned xs = base + kOffXs;
     bool ok = true;
     auto wait = [&](uint64_t* bar, unsigned parity) {
         if (ok) ok = mbar_wait_suspend(bar, parity);
@@ -242,21 +280,23 @@ __device__ __forceinline__ bool unit_loop(const PoolView& pv, const RaggedCall& 
     };
     auto write_state = [&]() {   // S in bf16, line n of the operand
 #pragma unroll
-        for (int c = 0; c < 8; ++c)
-            sts128(s_op + swz(t, c),
-                   make_uint4(pack_bf16(S[8 * c], S[8 * c + 1]), pack_bf16(S[8 * c + 2], S[8 * c + 3]),
-                              pack_bf16(S[8 * c + 4], S[8 * c + 5]),
-                              pack_bf16(S[8 * c + 6], S[8 * c + 7])));
+        for (int i = 0; i < 4; ++i)
+            sts128(s_op + swz(t, 4 * hf + i),
+                   make_uint4(pack_bf16(S[8 * i], S[8 * i + 1]), pack_bf16(S[8 * i + 2], S[8 * i + 3]),
+                              pack_bf16(S[8 * i + 4], S[8 * i + 5]),
+                              pack_bf16(S[8 * i + 6], S[8 * i + 7])));
         fence_proxy_async();
     };
     if constexpr (!STATE) {
         // M above the diagonal blocks stays zero
         const uint32_t zero[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-        for (int k = 0; k < 64; k += 8) tc::st8(tm + col_m(u) + k, zero);
+        for (int k = 0; k < 32; k += 8) tc::st8(tm + col_m(u) + 32 * hf + k, zero);
         tc::wait_st();
         write_state();
     }
-    if (t < kPT) ua.bad[t] = kL;
+    if (hf == 0 && t < kPT) ua.bad[t] = kL;
+    if (hf == 0 && t == 0) ua.any_bad = 0;
+    const bool leader = hf == 0 && t == 0;          // issues the unit's stores
 
     const long long tok0 = (long long)wk.run.t0 + (long long)wk.c0 * kL;
     const int left0 = wk.run.len - wk.c0 * kL;      // tokens from the segment's start
@@ -274,82 +314,65 @@ __device__ __forceinline__ bool unit_loop(const PoolView& pv, const RaggedCall& 
         float a = __fmul_rn(dt, A);
         if (a < kStepFloor) a = kStepFloor;         // a NaN stays
         if (t >= Lc) a = 0.0f;                      // dt is 0 there, A may be infinite
-        float r = a;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const float v = __shfl_up_sync(0xffffffffu, r, o);
-            if (lane >= o) r += v;
-        }
-        float q = __shfl_down_sync(0xffffffffu, a, 1);
+        float r = a, q = __shfl_down_sync(0xffffffffu, a, 1);
         if (lane == 31) q = 0.0f;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const float v = __shfl_down_sync(0xffffffffu, q, o);
-            if (lane + o < 32) q += v;
+            const float v = __shfl_up_sync(0xffffffffu, r, o);
+            const float z = __shfl_down_sync(0xffffffffu, q, o);
+            if (lane >= o) r += v;
+            if (lane + o < 32) q += z;
         }
         const float f = __fmul_rn(dt, expf(q));
-        ua.f[t] = f;
-        ua.r2[t] = __fmul_rn(r, kLog2e);
-        ua.dt[t] = dt;
-        if (lane == 31) ua.block[w] = r;
-        unit_sync(u);
-        float before = 0.0f, behind = 0.0f, total = 0.0f;
-        float between[3] = {0.0f, 0.0f, 0.0f};      // from block k's end to this block
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const float bs = ua.block[k];
-            total += bs;
-            if (k < w) before += bs;
-            if (k > w) behind += bs;
-#pragma unroll
-            for (int m = 0; m < 3; ++m)
-                if (m < k && k < w) between[m] += bs;
+        const float ri2 = __fmul_rn(r, kLog2e);
+        if (hf == 0) {
+            ua.f[t] = f;
+            if (lane == 31) ua.block[w] = r;
+        } else {
+            ua.r2[t] = __fsub_rn(ri2, __log2f(dt));
         }
+        unit_sync(u);
+        const float4 bs = *reinterpret_cast<const float4*>(ua.block);
+        // sums of the blocks behind this one and of all; what lies between an
+        // earlier block and this one
+        float behind = 0.0f;
+        if (w < 3) behind = bs.w;
+        if (w < 2) behind += bs.z;
+        if (w < 1) behind += bs.y;
+        const float b2 = w == 3 ? bs.z : 0.0f;                 // between block 1 and this
+        const float b1 = w == 3 ? bs.y + bs.z : w == 2 ? bs.y : 0.0f;   // ... block 0 ...
+        const float before = (w > 0 ? bs.x : 0.0f) + (w > 1 ? (w == 2 ? bs.y : bs.y + bs.z) : 0.0f);
+        if (!STATE && leader && c > 0) {
+            // y of the chunk before has been read from its x buffer
+            bulk_wait_read<0>();
+            mbar_arrive(&tl.x_empty[((c - 1) * nu + u) % kRingX]);
+        }
+        __syncwarp();
         const float wj = __fmul_rn(f, expf(behind));
-        const float lam = expf(total);
+        const float lam = expf((bs.x + bs.y) + (bs.z + bs.w));
         decay_all = __fmul_rn(decay_all, lam);
 
-        // ---- w X in two parts ----
+        // ---- w X in parts ----
         const int kx = c * nu + u, xslot = kx % kRingX;
         const unsigned xrow = base + kOffX + xslot * kTileX;
         wait(&tl.x_full[xslot], (kx / kRingX) & 1);
-        bool bad = false;
-        {
-            float2 acc = make_float2(0.0f, 0.0f);
-            const float2 w2 = make_float2(wj, wj), zero2 = make_float2(0.0f, 0.0f);
-            // the other unit's product has read the shared buffer
-            if (u == 0) {
-                if (c > 0) wait(&tl.ds_full[nu - 1], (c - 1) & 1);
-            } else {
-                wait(&tl.ds_full[0], c & 1);
-            }
-            const bool inside = t < Lc;
-#pragma unroll
-            for (int ch = 0; ch < 8; ++ch) {
-                uint4 xv = lds128(xrow + swz(t, ch));
-                if (!inside) xv = make_uint4(0, 0, 0, 0);
-                const uint32_t xw[4] = {xv.x, xv.y, xv.z, xv.w};
-                uint32_t hi[4], lo[4];
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const float2 x2 = unpack_bf16(xw[k]);
-                    acc = fma2(x2, zero2, acc);
-                    float2 v = mul2(x2, w2);
-                    if (!inside) v = zero2;          // w may be NaN
-                    hi[k] = pack_bf16(v.x, v.y);
-                    const float2 hv = unpack_bf16(hi[k]);
-                    const float2 d = add2(v, make_float2(-hv.x, -hv.y));
-                    lo[k] = pack_bf16(d.x, d.y);
-                }
-                sts128(xs_hi + swz(t, ch), make_uint4(hi[0], hi[1], hi[2], hi[3]));
-                sts128(xs_lo + swz(t, ch), make_uint4(lo[0], lo[1], lo[2], lo[3]));
-                if (!inside && !STATE) sts128(xrow + swz(t, ch), make_uint4(0, 0, 0, 0));
-            }
-            bad = !(acc.x + acc.y == 0.0f);
+        // the other unit's product has read the shared buffer
+        if (u == 0) {
+            if (c > 0) wait(&tl.ds_full[nu - 1], (c - 1) & 1);
+        } else {
+            wait(&tl.ds_full[0], c & 1);
         }
+        float fin;
+        if (Lc == kL)
+            fin = parts == 2 ? weigh_x<2, true, !STATE>(xrow, xs, t, hf, wj, true)
+                             : weigh_x<3, true, !STATE>(xrow, xs, t, hf, wj, true);
+        else
+            fin = weigh_x<3, false, !STATE>(xrow, xs, t, hf, wj, t < Lc);
+        const bool bad = !(fin == 0.0f);
         if (bad) {
             // rare: take the non-finite entries of this token out
-            for (int p = 0; p < kPT; ++p) {
+            ua.any_bad = 1;
+            for (int p = kPH * hf; p < kPH * hf + kPH; ++p) {
                 const unsigned at = swz(t, p >> 3) + (p & 7) * 2;
                 unsigned short v;
                 asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(xrow + at) : "memory");
@@ -357,157 +380,277 @@ __device__ __forceinline__ bool unit_loop(const PoolView& pv, const RaggedCall& 
                     atomicMin(&ua.bad[p], t);
                     const unsigned short z = 0;
                     asm volatile("st.shared.u16 [%0], %1;" :: "r"(xrow + at), "h"(z) : "memory");
-                    asm volatile("st.shared.u16 [%0], %1;" :: "r"(xs_hi + at), "h"(z) : "memory");
-                    asm volatile("st.shared.u16 [%0], %1;" :: "r"(xs_lo + at), "h"(z) : "memory");
+                    for (int k = 0; k < 3; ++k)
+                        asm volatile("st.shared.u16 [%0], %1;"
+                                     :: "r"(xs + k * kTileX + at), "h"(z) : "memory");
                 }
             }
         }
         __syncwarp();
         fence_proxy_async();
         mbar_arrive(&tl.xs_ready[u]);
-        if constexpr (STATE) mbar_arrive(&tl.x_empty[xslot]);
-        const bool any_bad = unit_any(u, bad);
 
         // ---- M ----
         if constexpr (!STATE) {
-            const float ri2 = __fmul_rn(r, kLog2e);
             wait(&tl.g_full, c & 1);
             tc::fence_after();
-            for (int k = 0; k <= w; ++k) {
-                const bool diag = k == w;
-                const float uk = diag ? 1.0f : expf(r + (k == 0 ? between[0] : k == 1 ? between[1]
-                                                                                 : between[2]));
+            for (int k = 0; k < w; ++k) {           // blocks before the diagonal one
+                const int j0 = 32 * k + 16 * hf;
+                float gv[16];
+                tc::ld16(tm + kColG + j0, gv);
+                const float uk = expf(r + (k == 0 ? b1 : k == 1 ? b2 : 0.0f));
+                const float2 u2 = make_float2(uk, uk);
+                float2 cf[8];
 #pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    const int j0 = 32 * k + 16 * half;
-                    float gv[16];
-                    tc::ld16(tm + kColG + j0, gv);
-                    float cf[16];
-                    if (!diag) {
-                        const float2 u2 = make_float2(uk, uk);
-#pragma unroll
-                        for (int m = 0; m < 16; m += 4) {
-                            const float4 fv = *reinterpret_cast<const float4*>(&ua.f[j0 + m]);
-                            const float2 c0 = mul2(make_float2(fv.x, fv.y), u2);
-                            const float2 c1 = mul2(make_float2(fv.z, fv.w), u2);
-                            cf[m] = c0.x; cf[m + 1] = c0.y; cf[m + 2] = c1.x; cf[m + 3] = c1.y;
-                        }
-                    } else {
-#pragma unroll
-                        for (int m = 0; m < 16; m += 4) {
-                            const float4 rv = *reinterpret_cast<const float4*>(&ua.r2[j0 + m]);
-                            const float4 dv = *reinterpret_cast<const float4*>(&ua.dt[j0 + m]);
-                            cf[m] = __fmul_rn(dv.x, ex2(__fsub_rn(ri2, rv.x)));
-                            cf[m + 1] = __fmul_rn(dv.y, ex2(__fsub_rn(ri2, rv.y)));
-                            cf[m + 2] = __fmul_rn(dv.z, ex2(__fsub_rn(ri2, rv.z)));
-                            cf[m + 3] = __fmul_rn(dv.w, ex2(__fsub_rn(ri2, rv.w)));
-                        }
-                    }
-                    tc::wait_ld(gv);
-                    uint32_t mw[8];
-#pragma unroll
-                    for (int m = 0; m < 16; m += 2) {
-                        float2 v = mul2(make_float2(gv[m], gv[m + 1]),
-                                        make_float2(cf[m], cf[m + 1]));
-                        if (diag) {                  // j > i: 0 whatever G holds there
-                            if (16 * half + m > lane) v.x = 0.0f;
-                            if (16 * half + m + 1 > lane) v.y = 0.0f;
-                        }
-                        mw[m / 2] = pack_bf16(v.x, v.y);
-                    }
-                    tc::st8(tm + col_m(u) + j0 / 2, mw);
+                for (int m = 0; m < 4; ++m) {
+                    const float4 fv = *reinterpret_cast<const float4*>(&ua.f[j0 + 4 * m]);
+                    cf[2 * m] = mul2(make_float2(fv.x, fv.y), u2);
+                    cf[2 * m + 1] = mul2(make_float2(fv.z, fv.w), u2);
                 }
+                tc::wait_ld(gv);
+                uint32_t mw[8];
+#pragma unroll
+                for (int m = 0; m < 8; ++m) {
+                    const float2 v = mul2(make_float2(gv[2 * m], gv[2 * m + 1]), cf[m]);
+                    mw[m] = pack_bf16(v.x, v.y);
+                }
+                tc::st8(tm + col_m(u) + j0 / 2, mw);
+            }
+            {
+                const int j0 = 32 * w + 16 * hf;
+                float gv[16], cf[16];
+                tc::ld16(tm + kColG + j0, gv);
+#pragma unroll
+                for (int m = 0; m < 16; m += 4) {
+                    const float4 rv = *reinterpret_cast<const float4*>(&ua.r2[j0 + m]);
+                    cf[m] = ex2(__fsub_rn(ri2, rv.x));
+                    cf[m + 1] = ex2(__fsub_rn(ri2, rv.y));
+                    cf[m + 2] = ex2(__fsub_rn(ri2, rv.z));
+                    cf[m + 3] = ex2(__fsub_rn(ri2, rv.w));
+                }
+                tc::wait_ld(gv);
+                tc::fence_before();
+                mbar_arrive(&tl.g_free);
+                uint32_t mw[8];
+                const int li = lane - 16 * hf;      // columns up to li are at or before i
+#pragma unroll
+                for (int m = 0; m < 16; m += 2) {
+                    // j > i: 0 whatever G holds there
+                    const float v0 = m <= li ? __fmul_rn(gv[m], cf[m]) : 0.0f;
+                    const float v1 = m + 1 <= li ? __fmul_rn(gv[m + 1], cf[m + 1]) : 0.0f;
+                    mw[m / 2] = pack_bf16(v0, v1);
+                }
+                tc::st8(tm + col_m(u) + j0 / 2, mw);
             }
             tc::wait_st();
-            tc::fence_before();
-            mbar_arrive(&tl.g_free);
         }
 
         // ---- state ----
+        wait(&tl.xs_ready[u], c & 1);               // every thread's any_bad is seen
+        const bool any_bad = ua.any_bad != 0;
         wait(&tl.ds_full[u], c & 1);
         tc::fence_after();
         {
             const float2 l2 = make_float2(lam, lam);
+            float d[2][16];
+            tc::ld16(tm + col_y1(u) + kPH * hf, d[0]);
+            tc::ld16(tm + col_y1(u) + kPH * hf + 16, d[1]);
+            tc::wait_ld(d[0]);
+            tc::after_wait(d[1]);
 #pragma unroll
-            for (int k = 0; k < kPT; k += 16) {
-                float d[16];
-                tc::ld16(tm + col_y1(u) + k, d);
-                tc::wait_ld(d);
-#pragma unroll
-                for (int m = 0; m < 16; m += 2) {
-                    const float2 v = fma2(l2, make_float2(S[k + m], S[k + m + 1]),
-                                          make_float2(d[m], d[m + 1]));
-                    S[k + m] = v.x;
-                    S[k + m + 1] = v.y;
-                }
+            for (int m = 0; m < kPH; m += 2) {
+                const float2 v = fma2(l2, make_float2(S[m], S[m + 1]),
+                                      make_float2(d[m / 16][m % 16], d[m / 16][m % 16 + 1]));
+                S[m] = v.x;
+                S[m + 1] = v.y;
             }
         }
+        tc::fence_before();
         if (any_bad) {
 #pragma unroll
-            for (int p = 0; p < kPT; ++p)
-                if (ua.bad[p] < kL) S[p] = __int_as_float(0x7fffffff);
+            for (int p = 0; p < kPH; ++p)
+                if (ua.bad[kPH * hf + p] < kL) S[p] = __int_as_float(0x7fffffff);
         }
-        tc::fence_before();
         if constexpr (!STATE) {
             mbar_arrive(&tl.m_ready[u]);
-            if (c + 1 < wk.nc) write_state();       // Y2 of this chunk has read the old one
 
             // ---- y ----
             const float ei = expf(r + before);
+            const float2 e2 = make_float2(ei, ei), D2 = make_float2(D, D);
             wait(&tl.y_full[u], c & 1);
             tc::fence_after();
-            const float2 e2 = make_float2(ei, ei), D2 = make_float2(D, D);
+            if (c + 1 < wk.nc) write_state();       // Y2 of this chunk has read the old one
 #pragma unroll
-            for (int k = 0; k < kPT; k += 16) {
+            for (int k = 0; k < kPH; k += 16) {
+                const int p = kPH * hf + k;
                 float y1[16], y2[16];
-                tc::ld16(tm + col_y1(u) + k, y1);
-                tc::ld16(tm + col_y2(u) + k, y2);
-                const uint4 xa = lds128(xrow + swz(t, k / 8)), xb = lds128(xrow + swz(t, k / 8 + 1));
+                tc::ld16(tm + col_y1(u) + p, y1);
+                tc::ld16(tm + col_y2(u) + p, y2);
+                const unsigned a0 = xrow + swz(t, p / 8), a1 = xrow + swz(t, p / 8 + 1);
+                const uint4 xa = lds128(a0), xb = lds128(a1);
                 tc::wait_ld(y1);
                 tc::after_wait(y2);
                 const uint32_t xw[8] = {xa.x, xa.y, xa.z, xa.w, xb.x, xb.y, xb.z, xb.w};
-                uint32_t yw[8];
+                float2 v[8];
 #pragma unroll
-                for (int m = 0; m < 16; m += 2) {
-                    float2 v = fma2(e2, make_float2(y2[m], y2[m + 1]), make_float2(y1[m], y1[m + 1]));
-                    v = fma2(D2, unpack_bf16(xw[m / 2]), v);
-                    if (any_bad) {
-                        if (ua.bad[k + m] <= t) v.x = __int_as_float(0x7fffffff);
-                        if (ua.bad[k + m + 1] <= t) v.y = __int_as_float(0x7fffffff);
-                    }
-                    yw[m / 2] = pack_bf16(v.x, v.y);
+                for (int m = 0; m < 8; ++m) {
+                    v[m] = fma2(e2, make_float2(y2[2 * m], y2[2 * m + 1]),
+                                make_float2(y1[2 * m], y1[2 * m + 1]));
+                    v[m] = fma2(D2, unpack_bf16(xw[m]), v[m]);
                 }
-                sts128(xrow + swz(t, k / 8), make_uint4(yw[0], yw[1], yw[2], yw[3]));
-                sts128(xrow + swz(t, k / 8 + 1), make_uint4(yw[4], yw[5], yw[6], yw[7]));
+                if (any_bad) {
+#pragma unroll
+                    for (int m = 0; m < 8; ++m) {
+                        if (ua.bad[p + 2 * m] <= t) v[m].x = __int_as_float(0x7fffffff);
+                        if (ua.bad[p + 2 * m + 1] <= t) v[m].y = __int_as_float(0x7fffffff);
+                    }
+                }
+                sts128(a0, make_uint4(pack_bf16(v[0].x, v[0].y), pack_bf16(v[1].x, v[1].y),
+                                      pack_bf16(v[2].x, v[2].y), pack_bf16(v[3].x, v[3].y)));
+                sts128(a1, make_uint4(pack_bf16(v[4].x, v[4].y), pack_bf16(v[5].x, v[5].y),
+                                      pack_bf16(v[6].x, v[6].y), pack_bf16(v[7].x, v[7].y)));
             }
             tc::fence_before();
-            unit_sync(u);
-            // rows of 128 bytes by 8 lanes each
-            if (ok) {
-                const int ch = t & 7;
-                __nv_bfloat16* yp = reinterpret_cast<__nv_bfloat16*>(rc.y)
-                                    + (tok0 + (long long)c * kL) * rc.ys + (long long)h * pv.P + p0
-                                    + ch * 8;
-                if (p0 + ch * 8 < pv.P) {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const int row = i * 16 + (t >> 3);
-                        if (row < Lc) {
-                            const uint4 v = lds128(xrow + swz(row, ch));
-                            __stcs(reinterpret_cast<uint4*>(yp + (long long)row * rc.ys), v);
-                        }
-                    }
-                }
-            }
             fence_proxy_async();
-            mbar_arrive(&tl.x_empty[xslot]);
+            unit_sync(u);
+            const int tok = (int)tok0 + c * kL;
+            if (Lc == kL) {
+                if (leader && ok) {
+                    tc::tma_store3(ymap, sm + kOffX + xslot * kTileX, p0, h, tok);
+                    bulk_commit();
+                }
+            } else if (ok) {
+                // the run's last tokens: rows of 128 bytes by 8 lanes each
+                const int id = hf * kL + t, ch = id & 7;
+                __nv_bfloat16* yp = reinterpret_cast<__nv_bfloat16*>(rc.y) + (long long)tok * rc.ys
+                                    + (long long)h * pv.P + p0 + ch * 8;
+                if (p0 + ch * 8 < pv.P)
+                    for (int row = id >> 3; row < Lc; row += kWg / 8)
+                        *reinterpret_cast<uint4*>(yp + (long long)row * rc.ys) =
+                            lds128(xrow + swz(row, ch));
+            }
         } else {
-            unit_sync(u);                           // `bad` is read by all before it is reset
+            unit_sync(u);                           // the x buffer and `bad` have been read
+            if (leader) mbar_arrive(&tl.x_empty[xslot]);
         }
-        if (any_bad && t < kPT) ua.bad[t] = kL;
+        if (any_bad && hf == 0 && t < kPT) {
+            ua.bad[t] = kL;
+            ua.any_bad = 0;
+        }
         dt = dt_next;
     }
+    if (!STATE && leader) bulk_wait_read<0>();      // the buffers outlive the stores
+    __syncwarp();
     return ok;
+}
+
+// ---------------------------------------------------------------------------
+// The products, one warp per sequence of them; lane 0 issues.  Every operand
+// address is a function of the chunk counter alone.
+// ---------------------------------------------------------------------------
+template <bool STATE>
+__device__ __forceinline__ int slot_b(int c) { return (STATE ? c : 2 * c + 1) % kRingCB; }
+template <bool STATE>
+__device__ __forceinline__ unsigned phase_b(int c)
+{
+    return (unsigned)((STATE ? c : 2 * c + 1) / kRingCB) & 1u;
+}
+__device__ __forceinline__ int slot_c(int c) { return 2 * c % kRingCB; }
+__device__ __forceinline__ unsigned phase_c(int c) { return (unsigned)(2 * c / kRingCB) & 1u; }
+
+// G = C B^T of every chunk.
+__device__ __forceinline__ bool issue_g(unsigned base, Tail& tl, uint32_t tmem, int nc,
+                                        int last_len, int halves, int lane)
+{
+    constexpr uint32_t kShape = tc::shape(128, 128, false, false);
+    for (int c = 0; c < nc; ++c) {
+        bool ok = mbar_wait_suspend(&tl.cb_full[slot_c(c)], phase_c(c));
+        ok = ok && mbar_wait_suspend(&tl.cb_full[slot_b<false>(c)], phase_b<false>(c));
+        if (ok && c > 0) ok = mbar_wait_suspend(&tl.g_free, (c - 1) & 1);
+        if (!__all_sync(0xffffffffu, ok)) return false;
+        const unsigned sc = base + slot_c(c) * kTileCB, sb = base + slot_b<false>(c) * kTileCB;
+        if (c == nc - 1 && last_len < kL) {
+            // lines of B past the run's end
+            for (int i = lane; i < (kL - last_len) * 8; i += 32)
+                for (int hf = 0; hf < halves; ++hf)
+                    sts128(sb + hf * kTileX + last_len * 128 + i * 16, make_uint4(0, 0, 0, 0));
+            fence_proxy_async();
+            __syncwarp();
+        }
+        if (lane == 0) {
+            mbar_arrive(&tl.b_ready);
+            tc::fence_after();
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                if (k < 4 || halves == 2) {
+                    const unsigned o = (k >> 2) * kTileX + (k & 3) * 32;
+                    tc::mma(tmem + kColG, tc::operand(sc + o), tc::operand(sb + o), kShape, k > 0);
+                }
+            tc::commit(&tl.g_full);
+            tc::commit(&tl.cb_empty[slot_c(c)]);
+            tc::commit(&tl.cb_empty[slot_b<false>(c)]);
+        }
+        __syncwarp();
+    }
+    return true;
+}
+
+// dS, Y2 and Y1 of unit U.
+template <bool STATE, int U>
+__device__ __forceinline__ bool issue_unit(unsigned base, Tail& tl, uint32_t tmem, int nc, int nu,
+                                           int last_len, int parts, int halves, int lane)
+{
+    constexpr uint32_t kShapeY = tc::shape(128, 64, false, true);
+    constexpr uint32_t kShapeS = tc::shape(128, 64, true, true);
+    const unsigned xs = base + kOffXs, so = base + kOffS + U * kTileX;
+    for (int c = 0; c < nc; ++c) {
+        const unsigned sb = base + slot_b<STATE>(c) * kTileCB;
+        bool ok = STATE ? mbar_wait_suspend(&tl.cb_full[slot_b<STATE>(c)], phase_b<STATE>(c))
+                        : mbar_wait_suspend(&tl.b_ready, c & 1);
+        ok = ok && mbar_wait_suspend(&tl.xs_ready[U], c & 1);
+        if (!__all_sync(0xffffffffu, ok)) return false;
+        // a partial chunk is always split in three
+        const bool three = parts == 3 || (c == nc - 1 && last_len < kL);
+        if (lane == 0) {
+            tc::fence_after();
+#pragma unroll
+            for (int part = 0; part < 3; ++part)
+                if (part < 2 || three)
+#pragma unroll
+                    for (int k = 0; k < kL / 16; ++k)
+                        tc::mma(tmem + col_y1(U), tc::operand(sb + k * 2048, kTileX),
+                                tc::operand(xs + part * kTileX + k * 2048), kShapeS,
+                                part + k > 0);
+            tc::commit(&tl.ds_full[U]);
+            tc::commit(&tl.cb_empty[slot_b<STATE>(c)]);
+            if constexpr (!STATE) {
+                const unsigned sc = base + slot_c(c) * kTileCB;
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    if (k < 4 || halves == 2)
+                        tc::mma(tmem + col_y2(U),
+                                tc::operand(sc + (k >> 2) * kTileX + (k & 3) * 32),
+                                tc::operand(so + k * 2048), kShapeY, k > 0);
+                tc::commit(&tl.cb_empty[slot_c(c)]);
+            }
+        }
+        __syncwarp();
+        if constexpr (!STATE) {
+            ok = mbar_wait_suspend(&tl.m_ready[U], c & 1);
+            if (!__all_sync(0xffffffffu, ok)) return false;
+            if (lane == 0) {
+                tc::fence_after();
+                const unsigned sx = base + kOffX + ((c * nu + U) % kRingX) * kTileX;
+#pragma unroll
+                for (int k = 0; k < kL / 16; ++k)
+                    tc::mma_ta(tmem + col_y1(U), tmem + col_m(U) + k * 8,
+                               tc::operand(sx + k * 2048), kShapeY, k > 0);
+                tc::commit(&tl.y_full[U]);
+            }
+            __syncwarp();
+        }
+    }
+    return true;
 }
 
 template <bool STATE>
@@ -515,9 +658,8 @@ __global__ void __launch_bounds__(kCThreadsTotal, 1)
 chunk_kernel(const __grid_constant__ PoolView pv, const __grid_constant__ RaggedCall rc,
              const __grid_constant__ ChunkMaps maps, int fmt)
 {
-    extern __shared__ unsigned char smem_raw[];
-    const unsigned raw = saddr(smem_raw);
-    unsigned char* sm = smem_raw + ((1024 - (raw & 1023)) & 1023);
+    extern __shared__ __align__(1024) unsigned char smem_raw[];
+    unsigned char* sm = smem_raw;
     const unsigned base = saddr(sm);
     Tail& tl = *reinterpret_cast<Tail*>(sm + kOffTail);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -555,11 +697,11 @@ chunk_kernel(const __grid_constant__ PoolView pv, const __grid_constant__ Ragged
     if (tid == 0) {
         for (int i = 0; i < kRingCB; ++i) {
             mbar_init(&tl.cb_full[i], 1);
-            mbar_init(&tl.cb_empty[i], 1);
+            mbar_init(&tl.cb_empty[i], STATE ? nu : nu + 1);
         }
         for (int i = 0; i < kRingX; ++i) {
             mbar_init(&tl.x_full[i], 1);
-            mbar_init(&tl.x_empty[i], kWg);
+            mbar_init(&tl.x_empty[i], 1);
         }
         for (int u = 0; u < 2; ++u) {
             mbar_init(&tl.xs_ready[u], kWg);
@@ -569,14 +711,15 @@ chunk_kernel(const __grid_constant__ PoolView pv, const __grid_constant__ Ragged
         }
         mbar_init(&tl.g_full, 1);
         mbar_init(&tl.g_free, kWg * nu);
-        mbar_init(&tl.drained, 1);
+        mbar_init(&tl.b_ready, 1);
+        for (int i = 0; i < 3; ++i) mbar_init(&tl.drained[i], 1);
         fence_proxy_async();
     }
     for (int i = tid; i < pv.H; i += kCThreadsTotal)
 #pragma unroll
         for (int u = 0; u < 2; ++u)
             if (pv.perm[i] == wk.h[u]) tl.pos[u] = i;
-    if (warp == 9) tc::alloc(&tl.tmem, kTmemCols);
+    if (warp == kElemWarps + 1) tc::alloc(&tl.tmem, kTmemCols);
     tc::fence_before();
     __syncthreads();
     tc::fence_after();
@@ -584,75 +727,106 @@ chunk_kernel(const __grid_constant__ PoolView pv, const __grid_constant__ Ragged
     const int halves = pv.N > 64 ? 2 : 1;           // 64-column halves of C and B
     bool ok = true;
 
-    if (warp < 8) {
-        const int u = warp >> 2, t = tid & (kWg - 1);
+    // the parts of w X that the stored state can show: fp32 rows take three
+    // (24 bits), rows of 16 bits and less two (16 bits)
+    int parts = 2;
+    for (int u = 0; u < nu; ++u)
+        if (fmt == SSQ_F32 || (fmt != SSQ_BF16 && tl.pos[u] >= pv.Hq)) parts = 3;
+
+    if (warp < kElemWarps) {
+        const int u = tid / kWg, t = tid & (kL - 1), hf = tid / kL & 1;
         const bool mine = u < nu;
         const int h = wk.h[u], p0 = wk.p0[u];
-        float S[kPT];
+        float S[kPH];       // S[p]: row p0 + 32 hf + p, entry t
         float decay_all = 1.0f;
-        // staging of the states at the ends: w X's buffer and the bf16 states'
+        // staging of the states at the ends: w X's buffers and the bf16 states'
         float* stage = reinterpret_cast<float*>(sm + (u == 0 ? kOffXs : kOffS));
-        const long long unit_state = ((long long)h * pv.P + p0) * pv.N;
+        const int ph = kPH * hf;
+        const long long unit_state = ((long long)h * pv.P + p0 + ph) * pv.N + t;
         const long long seg_state = ((long long)wk.b * rc.nseg + wk.seg) * pv.H * pv.P * pv.N;
 #pragma unroll
-        for (int p = 0; p < kPT; ++p) S[p] = 0.0f;
+        for (int p = 0; p < kPH; ++p) S[p] = 0.0f;
         if (mine && !STATE) {
             if (wk.nseg > 1) {
-                const float* src = rc.ws_state + seg_state + unit_state + t;
+                const float* src = rc.ws_state + seg_state + unit_state;
 #pragma unroll
-                for (int p = 0; p < kPT; ++p)
-                    if (t < pv.N && p0 + p < pv.P) S[p] = src[p * pv.N];
+                for (int p = 0; p < kPH; ++p)
+                    if (t < pv.N && p0 + ph + p < pv.P) S[p] = src[p * pv.N];
             } else if (!wk.run.fresh) {
-                unit_io_any(fmt, true, pv, wk.run.slot, rc.layer, tl.pos[u], p0, stage, t);
+                unit_io_any(fmt, true, pv, wk.run.slot, rc.layer, tl.pos[u], p0, stage,
+                            tid & (kWg - 1));
                 unit_sync(u);
 #pragma unroll
-                for (int p = 0; p < kPT; ++p)
-                    if (t < pv.N) S[p] = stage[p * pv.N + t];
+                for (int p = 0; p < kPH; ++p)
+                    if (t < pv.N) S[p] = stage[(ph + p) * pv.N + t];
             }
         }
         units_sync();       // the staging is read before the loops write there
-        if (mine) ok = unit_loop<STATE>(pv, rc, wk, base, tl, tmem, u, t, S, decay_all);
+        if (mine)
+            ok = unit_loop<STATE>(pv, rc, &maps.y, wk, sm, base, tl, tmem, u, t, hf, parts, S,
+                                  decay_all);
         units_sync();       // the loops are done with the staging
         if (mine && ok) {
             if constexpr (STATE) {
-                float* dst = rc.ws_state + seg_state + unit_state + t;
+                float* dst = rc.ws_state + seg_state + unit_state;
 #pragma unroll
-                for (int p = 0; p < kPT; ++p)
-                    if (t < pv.N && p0 + p < pv.P) dst[p * pv.N] = S[p];
-                if (t == 0 && p0 == 0)
+                for (int p = 0; p < kPH; ++p)
+                    if (t < pv.N && p0 + ph + p < pv.P) dst[p * pv.N] = S[p];
+                if (t == 0 && hf == 0 && p0 == 0)
                     rc.ws_decay[((long long)wk.b * rc.nseg + wk.seg) * pv.H + h] = decay_all;
             } else if (wk.seg + 1 == wk.nseg) {
 #pragma unroll
-                for (int p = 0; p < kPT; ++p)
-                    if (t < pv.N) stage[p * pv.N + t] = S[p];
+                for (int p = 0; p < kPH; ++p)
+                    if (t < pv.N) stage[(ph + p) * pv.N + t] = S[p];
                 unit_sync(u);
-                unit_io_any(fmt, false, pv, wk.run.slot, rc.layer, tl.pos[u], p0, stage, t);
+                unit_io_any(fmt, false, pv, wk.run.slot, rc.layer, tl.pos[u], p0, stage,
+                            tid & (kWg - 1));
             }
         }
-    } else if (warp == 8) {
+    } else if (warp == kElemWarps) {
         // ---- tensor copies ----
+        // In the order in which their buffers become free: C of the next
+        // chunk, x of unit 0, B (into C's buffer), x of unit 1.  What comes
+        // two chunks later is on its way to L2 meanwhile.
         if (lane == 0) {
             const int tok0 = wk.run.t0 + wk.c0 * kL;
             int k = 0, kx = 0;
+            auto load_cb = [&](const CUtensorMap* map, int tok) {
+                const int s = k % kRingCB;
+                if (k >= kRingCB && ok)
+                    ok = mbar_wait_suspend(&tl.cb_empty[s], (k / kRingCB - 1) & 1);
+                if (!ok) return;
+                mbar_arrive_tx(&tl.cb_full[s], (unsigned)(halves * kTileX));
+                for (int hf = 0; hf < halves; ++hf)
+                    tc::tma_load3(sm + s * kTileCB + hf * kTileX, map, hf * 64, wk.g, tok,
+                                  &tl.cb_full[s]);
+                ++k;
+            };
+            auto load_x = [&](int u, int tok) {
+                const int s = kx % kRingX;
+                if (kx >= kRingX && ok)
+                    ok = mbar_wait_suspend(&tl.x_empty[s], (kx / kRingX - 1) & 1);
+                if (!ok) return;
+                mbar_arrive_tx(&tl.x_full[s], kTileX);
+                tc::tma_load3(sm + kOffX + s * kTileX, &maps.x, wk.p0[u], wk.h[u], tok,
+                              &tl.x_full[s]);
+                ++kx;
+            };
             for (int c = 0; c < nc && ok; ++c) {
                 const int tok = tok0 + c * kL;
-                for (int which = STATE ? 1 : 0; which < 2 && ok; ++which, ++k) {   // C, then B
-                    const int s = k % kRingCB;
-                    if (k >= kRingCB) ok = mbar_wait_suspend(&tl.cb_empty[s], (k / kRingCB - 1) & 1);
-                    if (!ok) break;
-                    mbar_arrive_tx(&tl.cb_full[s], (unsigned)(halves * kTileX));
-                    for (int hf = 0; hf < halves; ++hf)
-                        tc::tma_load3(sm + s * kTileCB + hf * kTileX, which ? &maps.B : &maps.C,
-                                      hf * 64, wk.g, tok, &tl.cb_full[s]);
+                if (c + 2 < nc) {
+                    const int ahead = tok + 2 * kL;
+                    for (int u = 0; u < nu; ++u)
+                        tc::tma_prefetch3(&maps.x, wk.p0[u], wk.h[u], ahead);
+                    for (int hf = 0; hf < halves; ++hf) {
+                        if (!STATE) tc::tma_prefetch3(&maps.C, hf * 64, wk.g, ahead);
+                        tc::tma_prefetch3(&maps.B, hf * 64, wk.g, ahead);
+                    }
                 }
-                for (int u = 0; u < nu && ok; ++u, ++kx) {
-                    const int s = kx % kRingX;
-                    if (kx >= kRingX) ok = mbar_wait_suspend(&tl.x_empty[s], (kx / kRingX - 1) & 1);
-                    if (!ok) break;
-                    mbar_arrive_tx(&tl.x_full[s], kTileX);
-                    tc::tma_load3(sm + kOffX + s * kTileX, &maps.x, wk.p0[u], wk.h[u], tok,
-                                  &tl.x_full[s]);
-                }
+                if (!STATE) load_cb(&maps.C, tok);
+                load_x(0, tok);
+                load_cb(&maps.B, tok);
+                if (nu > 1) load_x(1, tok);
             }
             // no copy is in flight when the block ends, whatever happened
             for (int i = max(0, k - kRingCB); i < k; ++i)
@@ -663,107 +837,20 @@ chunk_kernel(const __grid_constant__ PoolView pv, const __grid_constant__ Ragged
         __syncwarp();
     } else {
         // ---- products ----
-        // Events in whatever order their operands become ready; the sums do
-        // not depend on it.  g, xs, m: chunks whose G, whose Y2 and dS, and
-        // whose Y1 have been issued.
-        constexpr uint32_t kShapeG = tc::shape(128, 128, false, false);
-        constexpr uint32_t kShapeY = tc::shape(128, 64, false, true);
-        constexpr uint32_t kShapeS = tc::shape(128, 64, true, true);
-        const int nk = halves * 4;                  // steps of 16 over d_state
-        int g = 0, xs[2] = {0, nu > 1 ? 0 : nc}, m[2] = {STATE ? nc : 0, STATE || nu == 1 ? nc : 0};
-        long long t0 = clock64();
         const int last_len = wk.run.len - (wk.c0 + nc - 1) * kL;
-        auto slot_c = [&](int c) { return (2 * c) % kRingCB; };
-        auto slot_b = [&](int c) { return (STATE ? c : 2 * c + 1) % kRingCB; };
-        auto par_c = [&](int c) { return (unsigned)((2 * c / kRingCB) & 1); };
-        auto par_b = [&](int c) { return (unsigned)(((STATE ? c : 2 * c + 1) / kRingCB) & 1); };
-        while (g < nc || xs[0] < nc || xs[1] < nc || m[0] < nc || m[1] < nc) {
-            int ev = -1;
-            if (lane == 0) {
-                for (int u = 0; u < 2 && ev < 0; ++u)
-                    if (m[u] < xs[u] && m[u] < nc && mbar_try(&tl.m_ready[u], m[u] & 1)) ev = u;
-                for (int u = 0; u < 2 && ev < 0; ++u)
-                    if (xs[u] < g && xs[u] < nc && mbar_try(&tl.xs_ready[u], xs[u] & 1)) ev = 2 + u;
-                if (ev < 0 && g < nc && (STATE || g == 0 || mbar_try(&tl.g_free, (g - 1) & 1))
-                    && (STATE || mbar_try(&tl.cb_full[slot_c(g)], par_c(g)))
-                    && mbar_try(&tl.cb_full[slot_b(g)], par_b(g)))
-                    ev = 4;
-            }
-            ev = __shfl_sync(0xffffffffu, ev, 0);
-            if (ev < 0) {
-                const bool late = clock64() - t0 > kWaitLimit;
-                if (__shfl_sync(0xffffffffu, (int)late, 0)) {
-                    ok = false;
-                    break;
-                }
-                __nanosleep(20);
-                continue;
-            }
-            t0 = clock64();
-            tc::fence_after();
-            if (ev == 4) {
-                const unsigned sb = base + slot_b(g) * kTileCB;
-                if (g == nc - 1 && last_len < kL) {
-                    // lines of B past the run's end
-                    mbar_try(&tl.cb_full[slot_b(g)], par_b(g));
-                    for (int i = lane; i < (kL - last_len) * 8; i += 32)
-                        for (int hf = 0; hf < halves; ++hf)
-                            sts128(sb + hf * kTileX + last_len * 128 + i * 16,
-                                   make_uint4(0, 0, 0, 0));
-                    fence_proxy_async();
-                    __syncwarp();
-                }
-                if (!STATE && lane == 0) {
-                    const unsigned sc = base + slot_c(g) * kTileCB;
-                    for (int k = 0; k < nk; ++k) {
-                        const unsigned o = (k >> 2) * kTileX + (k & 3) * 32;
-                        tc::mma(tmem + kColG, tc::operand(sc + o), tc::operand(sb + o), kShapeG,
-                                k > 0);
-                    }
-                    tc::commit(&tl.g_full);
-                }
-                ++g;
-            } else if (ev >= 2) {
-                const int u = ev - 2, c = xs[u];
-                const unsigned sb = base + slot_b(c) * kTileCB;
-                const bool both = xs[u ^ 1] > c;    // the chunk's C and B are done with
-                if (lane == 0) {
-                    if (!STATE) {
-                        const unsigned sc = base + slot_c(c) * kTileCB;
-                        const unsigned so = base + kOffS + u * kTileX;
-                        for (int k = 0; k < nk; ++k)
-                            tc::mma(tmem + col_y2(u),
-                                    tc::operand(sc + (k >> 2) * kTileX + (k & 3) * 32),
-                                    tc::operand(so + k * 2048), kShapeY, k > 0);
-                    }
-                    for (int part = 0; part < 2; ++part)
-                        for (int k = 0; k < kL / 16; ++k)
-                            tc::mma(tmem + col_y1(u), tc::operand(sb + k * 2048, kTileX),
-                                    tc::operand(base + kOffXs + part * kTileX + k * 2048), kShapeS,
-                                    part + k > 0);
-                    tc::commit(&tl.ds_full[u]);
-                    if (both) {
-                        if (!STATE) tc::commit(&tl.cb_empty[slot_c(c)]);
-                        tc::commit(&tl.cb_empty[slot_b(c)]);
-                    }
-                }
-                ++xs[u];
-            } else {
-                const int u = ev, c = m[u];
-                if (lane == 0) {
-                    const unsigned sx = base + kOffX + ((c * nu + u) % kRingX) * kTileX;
-                    for (int k = 0; k < kL / 16; ++k)
-                        tc::mma_ta(tmem + col_y1(u), tmem + col_m(u) + k * 8,
-                                   tc::operand(sx + k * 2048), kShapeY, k > 0);
-                    tc::commit(&tl.y_full[u]);
-                }
-                ++m[u];
-            }
+        if (warp == kElemWarps + 1) {
+            if constexpr (!STATE)
+                ok = issue_g(base, tl, tmem, nc, last_len, halves, lane);
+        } else if (warp == kElemWarps + 2) {
+            ok = issue_unit<STATE, 0>(base, tl, tmem, nc, nu, last_len, parts, halves, lane);
+        } else if (nu > 1) {
+            ok = issue_unit<STATE, 1>(base, tl, tmem, nc, nu, last_len, parts, halves, lane);
         }
         // the products are complete before the memory they use goes away
         if (lane == 0) {
-            tc::commit(&tl.drained);
-            mbar_wait_suspend(&tl.drained, 0);
+            uint64_t* bar = &tl.drained[warp - kElemWarps - 1];
+            tc::commit(bar);
+            mbar_wait_suspend(bar, 0);
         }
         __syncwarp();
     }
@@ -771,7 +858,7 @@ chunk_kernel(const __grid_constant__ PoolView pv, const __grid_constant__ Ragged
     tc::fence_before();
     __syncthreads();
     tc::fence_after();
-    if (warp == 9) tc::dealloc(tmem, kTmemCols);
+    if (warp == kElemWarps + 1) tc::dealloc(tmem, kTmemCols);
 }
 
 // ---------------------------------------------------------------------------
@@ -926,6 +1013,7 @@ cudaError_t launch_ragged_chunks(const PoolView& pv, const RaggedCall& rc, int f
     cudaError_t e = make_map(&maps.x, rc.x, pv.P, pv.H, rc.total, rc.xs);
     if (e == cudaSuccess) e = make_map(&maps.B, rc.B, pv.N, pv.G, rc.total, rc.Bs);
     if (e == cudaSuccess) e = make_map(&maps.C, rc.C, pv.N, pv.G, rc.total, rc.Cs);
+    if (e == cudaSuccess) e = make_map(&maps.y, rc.y, pv.P, pv.H, rc.total, rc.ys);
     if (e == cudaSuccess && rc.nseg > 1) {
         e = launch_pass<true>(pv, rc, maps, fmt, st);
         if (e == cudaSuccess) e = join(pv, rc, fmt, st);
