@@ -577,14 +577,15 @@ __device__ __forceinline__ bool issue_g(unsigned base, Tail& tl, uint32_t tmem, 
             fence_proxy_async();
             __syncwarp();
         }
-        if (lane == 0) {
+        if (tc::elect()) {
             mbar_arrive(&tl.b_ready);
             tc::fence_after();
+            const uint64_t dc = tc::operand(sc), db = tc::operand(sb);
 #pragma unroll
             for (int k = 0; k < 8; ++k)
                 if (k < 4 || halves == 2) {
-                    const unsigned o = (k >> 2) * kTileX + (k & 3) * 32;
-                    tc::mma(tmem + kColG, tc::operand(sc + o), tc::operand(sb + o), kShape, k > 0);
+                    const unsigned o = ((k >> 2) * kTileX + (k & 3) * 32) >> 4;
+                    tc::mma(tmem + kColG, dc + o, db + o, kShape, k > 0);
                 }
             tc::commit(&tl.g_full);
             tc::commit(&tl.cb_empty[slot_c(c)]);
@@ -611,26 +612,25 @@ __device__ __forceinline__ bool issue_unit(unsigned base, Tail& tl, uint32_t tme
         if (!__all_sync(0xffffffffu, ok)) return false;
         // a partial chunk is always split in three
         const bool three = parts == 3 || (c == nc - 1 && last_len < kL);
-        if (lane == 0) {
+        if (tc::elect()) {
             tc::fence_after();
+            const uint64_t db = tc::operand(sb, kTileX), dx = tc::operand(xs);
 #pragma unroll
             for (int part = 0; part < 3; ++part)
                 if (part < 2 || three)
 #pragma unroll
                     for (int k = 0; k < kL / 16; ++k)
-                        tc::mma(tmem + col_y1(U), tc::operand(sb + k * 2048, kTileX),
-                                tc::operand(xs + part * kTileX + k * 2048), kShapeS,
-                                part + k > 0);
+                        tc::mma(tmem + col_y1(U), db + k * 128, dx + (part * kTileX >> 4) + k * 128,
+                                kShapeS, part + k > 0);
             tc::commit(&tl.ds_full[U]);
             tc::commit(&tl.cb_empty[slot_b<STATE>(c)]);
             if constexpr (!STATE) {
-                const unsigned sc = base + slot_c(c) * kTileCB;
+                const uint64_t dc = tc::operand(base + slot_c(c) * kTileCB), ds = tc::operand(so);
 #pragma unroll
                 for (int k = 0; k < 8; ++k)
                     if (k < 4 || halves == 2)
-                        tc::mma(tmem + col_y2(U),
-                                tc::operand(sc + (k >> 2) * kTileX + (k & 3) * 32),
-                                tc::operand(so + k * 2048), kShapeY, k > 0);
+                        tc::mma(tmem + col_y2(U), dc + (((k >> 2) * kTileX + (k & 3) * 32) >> 4),
+                                ds + k * 128, kShapeY, k > 0);
                 tc::commit(&tl.cb_empty[slot_c(c)]);
             }
         }
@@ -638,13 +638,14 @@ __device__ __forceinline__ bool issue_unit(unsigned base, Tail& tl, uint32_t tme
         if constexpr (!STATE) {
             ok = mbar_wait_suspend(&tl.m_ready[U], c & 1);
             if (!__all_sync(0xffffffffu, ok)) return false;
-            if (lane == 0) {
+            if (tc::elect()) {
                 tc::fence_after();
-                const unsigned sx = base + kOffX + ((c * nu + U) % kRingX) * kTileX;
+                const uint64_t dx =
+                    tc::operand(base + kOffX + ((c * nu + U) % kRingX) * kTileX);
 #pragma unroll
                 for (int k = 0; k < kL / 16; ++k)
-                    tc::mma_ta(tmem + col_y1(U), tmem + col_m(U) + k * 8,
-                               tc::operand(sx + k * 2048), kShapeY, k > 0);
+                    tc::mma_ta(tmem + col_y1(U), tmem + col_m(U) + k * 8, dx + k * 128, kShapeY,
+                               k > 0);
                 tc::commit(&tl.y_full[U]);
             }
             __syncwarp();
@@ -847,7 +848,7 @@ chunk_kernel(const __grid_constant__ PoolView pv, const __grid_constant__ Ragged
             ok = issue_unit<STATE, 1>(base, tl, tmem, nc, nu, last_len, parts, halves, lane);
         }
         // the products are complete before the memory they use goes away
-        if (lane == 0) {
+        if (tc::elect()) {
             uint64_t* bar = &tl.drained[warp - kElemWarps - 1];
             tc::commit(bar);
             mbar_wait_suspend(bar, 0);

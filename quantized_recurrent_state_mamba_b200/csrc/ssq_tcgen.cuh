@@ -100,6 +100,14 @@ __device__ __forceinline__ void mma_ta(uint32_t d, uint32_t a, uint64_t b, uint3
                  " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n"
                  :: "r"(d), "r"(a), "l"(b), "r"(idesc), "r"((unsigned)acc) : "memory");
 }
+// True in one thread of the (converged) warp, always the same one.
+__device__ __forceinline__ bool elect()
+{
+    unsigned r;
+    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n"
+                 : "=r"(r));
+    return r != 0;
+}
 // One arrival on `bar` when this thread's products so far have completed.
 __device__ __forceinline__ void commit(uint64_t* bar)
 {
