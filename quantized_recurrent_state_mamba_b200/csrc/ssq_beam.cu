@@ -421,7 +421,8 @@ cudaError_t launch_one(const BeamCall& bc, int cs, cudaStream_t st)
 {
     auto kern = beam_kernel<TYPE, KP>;
     constexpr int smem = (int)(sizeof(BeamShared) + sizeof(FinalShared));
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    thread_local int done = -1;
+    cudaError_t e = allow_smem(kern, smem, &done);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(bc.batch * cs));

@@ -219,12 +219,56 @@ struct Work {
 // ---------------------------------------------------------------------------
 constexpr int kPH = kPT / 2;
 
-// Token t's part of w X: NP bf16 parts (hi, the rest, the rest of that) to
-// shared memory.  With FULL the chunk has 128 tokens; otherwise tokens that
-// are not `inside` become zero.  Returns a sum that is 0 unless an x is not
-// finite.
-template <int NP, bool FULL, bool ZERO_X>
-__device__ __forceinline__ float weigh_x(unsigned xrow, unsigned xs, int t, int hf, float wj,
+// bf16 pairs: products and sums rounded once
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b)
+{
+    uint32_t r;
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+__device__ __forceinline__ uint32_t fma_bf16x2(uint32_t a, uint32_t b, uint32_t c)
+{
+    uint32_t r;
+    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+    return r;
+}
+
+// Token t's part of w X as bf16 parts to shared memory.  Both return whether
+// an x is not finite (x * 0 summed: NaN).
+//
+// Two parts, in bf16 arithmetic: with w = w1 + w2 (w1 its rounding, w2 that of
+// the rest), hi = rn(x w1), e = x w1 - hi, which a fused multiply-add gives
+// exactly, and lo = rn(x w2 + e).  What is left out is 2^-17 of w and the
+// rounding of lo, 2^-9 of a term that is at most 2^-8 of the product.
+__device__ __forceinline__ bool weigh_x2(unsigned xrow, unsigned xs, int t, int hf, float wj)
+{
+    const uint32_t w1 = pack_bf16(wj, wj);
+    const float rest = __fsub_rn(wj, unpack_bf16(w1).x);
+    const uint32_t w2 = pack_bf16(rest, rest);
+    uint32_t acc = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const unsigned at = swz(t, 4 * hf + i);
+        const uint4 xv = lds128(xrow + at);
+        const uint32_t xw[4] = {xv.x, xv.y, xv.z, xv.w};
+        uint32_t hi[4], lo[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            acc = fma_bf16x2(xw[k], 0, acc);
+            hi[k] = mul_bf16x2(xw[k], w1);
+            lo[k] = fma_bf16x2(xw[k], w2, fma_bf16x2(xw[k], w1, hi[k] ^ 0x80008000u));
+        }
+        sts128(xs + at, make_uint4(hi[0], hi[1], hi[2], hi[3]));
+        sts128(xs + kTileX + at, make_uint4(lo[0], lo[1], lo[2], lo[3]));
+    }
+    return (acc & 0x7fff7fffu) != 0;
+}
+
+// Three parts, in fp32: rn(w x), the rounding of the rest, and of the rest of
+// that.  Without FULL, tokens that are not `inside` the run become zero, in
+// x's buffer too.
+template <bool FULL, bool ZERO_X>
+__device__ __forceinline__ bool weigh_x3(unsigned xrow, unsigned xs, int t, int hf, float wj,
                                          bool inside)
 {
     const float2 w2 = make_float2(wj, wj), zero2 = make_float2(0.0f, 0.0f);
@@ -235,7 +279,7 @@ __device__ __forceinline__ float weigh_x(unsigned xrow, unsigned xs, int t, int 
         uint4 xv = lds128(xrow + at);
         if (!FULL && !inside) xv = make_uint4(0, 0, 0, 0);
         const uint32_t xw[4] = {xv.x, xv.y, xv.z, xv.w};
-        uint32_t part[NP][4];
+        uint32_t part[3][4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
             const float2 x2 = unpack_bf16(xw[k]);
@@ -243,21 +287,21 @@ __device__ __forceinline__ float weigh_x(unsigned xrow, unsigned xs, int t, int 
             float2 v = mul2(x2, w2);
             if (!FULL && !inside) v = zero2;         // w may be NaN
 #pragma unroll
-            for (int q = 0; q < NP; ++q) {
+            for (int q = 0; q < 3; ++q) {
                 part[q][k] = pack_bf16(v.x, v.y);
-                if (q + 1 < NP) {
+                if (q < 2) {
                     const float2 h = unpack_bf16(part[q][k]);
                     v = fma2(h, make_float2(-1.0f, -1.0f), v);   // exact
                 }
             }
         }
 #pragma unroll
-        for (int q = 0; q < NP; ++q)
+        for (int q = 0; q < 3; ++q)
             sts128(xs + q * kTileX + at,
                    make_uint4(part[q][0], part[q][1], part[q][2], part[q][3]));
         if (!FULL && ZERO_X && !inside) sts128(xrow + at, make_uint4(0, 0, 0, 0));
     }
-    return acc.x + acc.y;
+    return !(acc.x + acc.y == 0.0f);
 }
 
 template <bool STATE>
@@ -275,7 +319,7 @@ __device__ __forceinline__ bool unit_loop(const PoolView& pv, const RaggedCall& 
     const unsigned xs = base + kOffXs;
     bool ok = true;
     auto wait = [&](uint64_t* bar, unsigned parity) {
-        if (ok) ok = mbar_wait_suspend(bar, parity);
+        if (ok) ok = tc::wait_phase(bar, parity);
         __syncwarp();               // the tensor-memory accesses are the whole warp's
     };
     auto write_state = [&]() {   // S in bf16, line n of the operand
@@ -285,7 +329,7 @@ __device__ __forceinline__ bool unit_loop(const PoolView& pv, const RaggedCall& 
                    make_uint4(pack_bf16(S[8 * i], S[8 * i + 1]), pack_bf16(S[8 * i + 2], S[8 * i + 3]),
                               pack_bf16(S[8 * i + 4], S[8 * i + 5]),
                               pack_bf16(S[8 * i + 6], S[8 * i + 7])));
-        fence_proxy_async();
+        // (the fence before the next xs_ready publishes it)
     };
     if constexpr (!STATE) {
         // M above the diagonal blocks stays zero
@@ -362,13 +406,9 @@ __device__ __forceinline__ bool unit_loop(const PoolView& pv, const RaggedCall& 
         } else {
             wait(&tl.ds_full[0], c & 1);
         }
-        float fin;
-        if (Lc == kL)
-            fin = parts == 2 ? weigh_x<2, true, !STATE>(xrow, xs, t, hf, wj, true)
-                             : weigh_x<3, true, !STATE>(xrow, xs, t, hf, wj, true);
-        else
-            fin = weigh_x<3, false, !STATE>(xrow, xs, t, hf, wj, t < Lc);
-        const bool bad = !(fin == 0.0f);
+        const bool bad = Lc < kL ? weigh_x3<false, !STATE>(xrow, xs, t, hf, wj, t < Lc)
+                         : parts == 2 ? weigh_x2(xrow, xs, t, hf, wj)
+                                      : weigh_x3<true, !STATE>(xrow, xs, t, hf, wj, true);
         if (bad) {
             // rare: take the non-finite entries of this token out
             ua.any_bad = 1;
@@ -564,9 +604,9 @@ __device__ __forceinline__ bool issue_g(unsigned base, Tail& tl, uint32_t tmem, 
 {
     constexpr uint32_t kShape = tc::shape(128, 128, false, false);
     for (int c = 0; c < nc; ++c) {
-        bool ok = mbar_wait_suspend(&tl.cb_full[slot_c(c)], phase_c(c));
-        ok = ok && mbar_wait_suspend(&tl.cb_full[slot_b<false>(c)], phase_b<false>(c));
-        if (ok && c > 0) ok = mbar_wait_suspend(&tl.g_free, (c - 1) & 1);
+        bool ok = tc::wait_phase(&tl.cb_full[slot_c(c)], phase_c(c));
+        ok = ok && tc::wait_phase(&tl.cb_full[slot_b<false>(c)], phase_b<false>(c));
+        if (ok && c > 0) ok = tc::wait_phase(&tl.g_free, (c - 1) & 1);
         if (!__all_sync(0xffffffffu, ok)) return false;
         const unsigned sc = base + slot_c(c) * kTileCB, sb = base + slot_b<false>(c) * kTileCB;
         if (c == nc - 1 && last_len < kL) {
@@ -606,9 +646,9 @@ __device__ __forceinline__ bool issue_unit(unsigned base, Tail& tl, uint32_t tme
     const unsigned xs = base + kOffXs, so = base + kOffS + U * kTileX;
     for (int c = 0; c < nc; ++c) {
         const unsigned sb = base + slot_b<STATE>(c) * kTileCB;
-        bool ok = STATE ? mbar_wait_suspend(&tl.cb_full[slot_b<STATE>(c)], phase_b<STATE>(c))
-                        : mbar_wait_suspend(&tl.b_ready, c & 1);
-        ok = ok && mbar_wait_suspend(&tl.xs_ready[U], c & 1);
+        bool ok = STATE ? tc::wait_phase(&tl.cb_full[slot_b<STATE>(c)], phase_b<STATE>(c))
+                        : tc::wait_phase(&tl.b_ready, c & 1);
+        ok = ok && tc::wait_phase(&tl.xs_ready[U], c & 1);
         if (!__all_sync(0xffffffffu, ok)) return false;
         // a partial chunk is always split in three
         const bool three = parts == 3 || (c == nc - 1 && last_len < kL);
@@ -636,7 +676,7 @@ __device__ __forceinline__ bool issue_unit(unsigned base, Tail& tl, uint32_t tme
         }
         __syncwarp();
         if constexpr (!STATE) {
-            ok = mbar_wait_suspend(&tl.m_ready[U], c & 1);
+            ok = tc::wait_phase(&tl.m_ready[U], c & 1);
             if (!__all_sync(0xffffffffu, ok)) return false;
             if (tc::elect()) {
                 tc::fence_after();
@@ -795,7 +835,7 @@ chunk_kernel(const __grid_constant__ PoolView pv, const __grid_constant__ Ragged
             auto load_cb = [&](const CUtensorMap* map, int tok) {
                 const int s = k % kRingCB;
                 if (k >= kRingCB && ok)
-                    ok = mbar_wait_suspend(&tl.cb_empty[s], (k / kRingCB - 1) & 1);
+                    ok = tc::wait_phase(&tl.cb_empty[s], (k / kRingCB - 1) & 1);
                 if (!ok) return;
                 mbar_arrive_tx(&tl.cb_full[s], (unsigned)(halves * kTileX));
                 for (int hf = 0; hf < halves; ++hf)
@@ -806,7 +846,7 @@ chunk_kernel(const __grid_constant__ PoolView pv, const __grid_constant__ Ragged
             auto load_x = [&](int u, int tok) {
                 const int s = kx % kRingX;
                 if (kx >= kRingX && ok)
-                    ok = mbar_wait_suspend(&tl.x_empty[s], (kx / kRingX - 1) & 1);
+                    ok = tc::wait_phase(&tl.x_empty[s], (kx / kRingX - 1) & 1);
                 if (!ok) return;
                 mbar_arrive_tx(&tl.x_full[s], kTileX);
                 tc::tma_load3(sm + kOffX + s * kTileX, &maps.x, wk.p0[u], wk.h[u], tok,
@@ -831,9 +871,9 @@ chunk_kernel(const __grid_constant__ PoolView pv, const __grid_constant__ Ragged
             }
             // no copy is in flight when the block ends, whatever happened
             for (int i = max(0, k - kRingCB); i < k; ++i)
-                mbar_wait_suspend(&tl.cb_full[i % kRingCB], (i / kRingCB) & 1);
+                tc::wait_phase(&tl.cb_full[i % kRingCB], (i / kRingCB) & 1);
             for (int i = max(0, kx - kRingX); i < kx; ++i)
-                mbar_wait_suspend(&tl.x_full[i % kRingX], (i / kRingX) & 1);
+                tc::wait_phase(&tl.x_full[i % kRingX], (i / kRingX) & 1);
         }
         __syncwarp();
     } else {
@@ -851,7 +891,7 @@ chunk_kernel(const __grid_constant__ PoolView pv, const __grid_constant__ Ragged
         if (tc::elect()) {
             uint64_t* bar = &tl.drained[warp - kElemWarps - 1];
             tc::commit(bar);
-            mbar_wait_suspend(bar, 0);
+            tc::wait_phase(bar, 0);
         }
         __syncwarp();
     }
@@ -981,8 +1021,8 @@ template <bool STATE>
 cudaError_t launch_pass(const PoolView& pv, const RaggedCall& rc, const ChunkMaps& maps, int fmt,
                         cudaStream_t st)
 {
-    cudaError_t e = cudaFuncSetAttribute(chunk_kernel<STATE>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+    thread_local int done = -1;
+    cudaError_t e = allow_smem(chunk_kernel<STATE>, kSmemBytes, &done);
     if (e != cudaSuccess) return e;
     const long long blocks = (long long)chunk_pairs(pv.H, pv.P, pv.G) * rc.batch * rc.nseg;
     if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;

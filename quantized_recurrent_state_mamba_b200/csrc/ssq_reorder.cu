@@ -190,8 +190,9 @@ cudaError_t launch_reorder(ReorderCall rc, cudaStream_t st)
     }
     const long long items = per * rc.batch;
     const int smem = kStages * chunk * rc.beams;
-    cudaError_t e = cudaFuncSetAttribute(reorder_kernel,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    static_assert(kStages * kStageBudget <= 227 * 1024, "shared memory");
+    thread_local int done = -1;
+    cudaError_t e = allow_smem(reorder_kernel, kStages * kStageBudget, &done);
     if (e != cudaSuccess) return e;
     const unsigned grid = (unsigned)(items < kSMs ? items : kSMs);
     reorder_kernel<<<grid, 32, smem, st>>>(rc);

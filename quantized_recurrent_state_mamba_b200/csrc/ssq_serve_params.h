@@ -9,6 +9,19 @@ namespace ssq {
 // SMs of the one GPU that the library is built for (B200).
 constexpr int kSMs = 148;
 
+// Allow `kernel` this much dynamic shared memory, once per device and thread
+// (`done`: the caller's thread_local, initially -1).
+template <typename K>
+inline cudaError_t allow_smem(K kernel, int bytes, int* done)
+{
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess || *done == dev) return e;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) *done = dev;
+    return e;
+}
+
 struct BeamCall {
     int batch, beams, vocab, nsel, done_token;
     int type;                 // ssq_dtype

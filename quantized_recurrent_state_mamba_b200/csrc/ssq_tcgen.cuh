@@ -32,6 +32,20 @@ __device__ __forceinline__ void fence_after()
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
 }
 
+// Wait for the phase of the given parity.  The test itself suspends the
+// thread for a bounded time and wakes it when the phase completes, so a
+// waiting warp takes few issue slots (with a time hint the same wait was
+// seen to poll: a third of the chunk kernel's instructions).  False after
+// about a second.
+__device__ __forceinline__ bool wait_phase(uint64_t* bar, unsigned parity)
+{
+    if (mbar_try(bar, parity)) return true;
+    const long long t0 = clock64();
+    while (!mbar_try(bar, parity))
+        if (clock64() - t0 > kWaitLimit) return false;
+    return true;
+}
+
 // 16 columns of this thread's TMEM lane; valid after wait_ld on the same array.
 __device__ __forceinline__ void ld16(uint32_t taddr, float (&v)[16])
 {

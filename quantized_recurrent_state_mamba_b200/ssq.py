@@ -407,8 +407,45 @@ def ssq_damp_pool_error(cfg: DampConfig, pool, stream=None) -> int:
 def _on(device, **tensors):
     """All given tensors live on `device`."""
     for name, t in tensors.items():
-        if isinstance(t, torch.Tensor) and t.device != device:
-            raise ValueError(f"{name}: on {t.device}, the pool or logits on {device}")
+        if t is not None and isinstance(t, torch.Tensor) and t.device != device:
+            raise ValueError(f"{name}: on {t.device}, the other tensors on {device}")
+
+
+def _pool_bytes(cfg):
+    """layout.pool_bytes, kept in the configuration for as long as its fields
+    stay the same (these calls are short)."""
+    key = bytes(cfg.c)
+    kept = cfg.__dict__.get("_kept")
+    if kept is None or kept[0] != key:
+        layout = ssq_damp_pool_layout(cfg) if isinstance(cfg, DampConfig) else \
+            ssq_pool_layout(cfg)[0]
+        kept = cfg.__dict__["_kept"] = (key, layout["pool_bytes"])
+    return kept[1]
+
+
+class _Launch:
+    """The calling thread's device and stream for a call on tensors of
+    `device`: the stream given, else the device's current stream."""
+
+    def __init__(self, device, stream):
+        index = device.index
+        self.guard = None
+        if index != torch.cuda.current_device():
+            self.guard = torch.cuda.device(index)
+        if stream is None:
+            self.stream = torch._C._cuda_getCurrentRawStream(index)
+        else:
+            self.stream = _stream(stream)
+
+    def __enter__(self):
+        if self.guard is not None:
+            self.guard.__enter__()
+        return self.stream
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+        return False
 
 
 def _token_ptr(t, name, dtype, total, shape):
@@ -420,14 +457,15 @@ def _token_ptr(t, name, dtype, total, shape):
         raise ValueError(f"{name}: expected a CUDA tensor")
     if t.dtype != dtype:
         raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
-    if tuple(t.shape) != (total, *shape):
+    if t.shape != (total, *shape):
         raise ValueError(f"{name}: shape {tuple(t.shape)}, need {(total, *shape)}")
+    strides = t.stride()
     inner = 1
-    for k in range(len(shape) - 1, -1, -1):
-        if shape[k] > 1 and t.stride(k + 1) != inner:
+    for k in range(len(shape), 0, -1):
+        if strides[k] != inner and shape[k - 1] > 1:
             raise ValueError(f"{name}: the entries of one token must be contiguous")
-        inner *= shape[k]
-    return t.data_ptr(), (t.stride(0) if total > 1 else inner)
+        inner *= shape[k - 1]
+    return t.data_ptr(), (strides[0] if total > 1 else inner)
 
 
 def ssq_prefill_ragged_workspace(cfg: Config, batch, max_len) -> int:
@@ -451,13 +489,15 @@ def ssq_prefill_ragged(cfg: Config, pool, slot_idx, batch, layer, cu_tokens, max
     (int32 [batch+1]).  x/y [total][H][P], B/C [total][G][N] in bfloat16,
     float16 or float32 (token strides free), dt [total][H], A/D [H] float32;
     fresh uint8 [batch] marks requests that start from the zero state."""
-    H, P, N, G = cfg.nheads, cfg.headdim, cfg.d_state, cfg.ngroups
+    c = cfg.c
+    H, P, N, G = c.nheads, c.headdim, c.d_state, c.ngroups
     f = torch.float32
-    pp = _pool_ptr(cfg, pool)
+    pp = _ptr(pool, "pool", torch.uint8, _pool_bytes(cfg))
     if not isinstance(x, torch.Tensor) or x.dtype not in _ACT_TYPES:
         raise TypeError("x: expected a bfloat16, float16 or float32 tensor")
-    _on(x.device, pool=pool, slot_idx=slot_idx, cu_tokens=cu_tokens, B=B, C=C, dt=dt, A=A, D=D,
-        y=y, fresh=fresh, workspace=workspace)
+    dev = x.device
+    _on(dev, pool=pool, slot_idx=slot_idx, cu_tokens=cu_tokens, B=B, C=C, dt=dt, A=A, D=D, y=y,
+        fresh=fresh, workspace=workspace)
     total = x.shape[0]
     tok = ssq_tokens()
     tok.type = _ACT_TYPES[x.dtype]
@@ -467,18 +507,17 @@ def ssq_prefill_ragged(cfg: Config, pool, slot_idx, batch, layer, cu_tokens, max
     tok.C, tok.C_stride = _token_ptr(C, "C", x.dtype, total, (G, N))
     tok.dt, tok.dt_stride = _token_ptr(dt, "dt", f, total, (H,))
     tok.y, tok.y_stride = _token_ptr(y, "y", x.dtype, total, (H, P))
-    ws = 0
+    wp, ws = None, 0
     if workspace is not None:
         if not isinstance(workspace, torch.Tensor) or not workspace.is_contiguous():
             raise ValueError("workspace: expected a contiguous CUDA tensor")
-        ws = workspace.numel() * workspace.element_size()
-    with torch.cuda.device(x.device):
+        wp, ws = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    with _Launch(dev, stream) as st:
         _check(_lib.ssq_prefill_ragged(
             cfg.ref, pp, _slots(slot_idx, batch), batch, layer,
             _ptr(cu_tokens, "cu_tokens", torch.int32, batch + 1), max_len,
             _ptr(fresh, "fresh", torch.uint8, batch, allow_none=True), ctypes.byref(tok),
-            _ptr(A, "A", f, H), _ptr(D, "D", f, H),
-            workspace.data_ptr() if ws else None, ws, _stream(stream)))
+            _ptr(A, "A", f, H), _ptr(D, "D", f, H), wp, ws, st))
 
 
 def ssq_beam_select(logits, scores, done=None, done_token=0, nsel=None, out=None, stream=None):
@@ -495,10 +534,11 @@ def ssq_beam_select(logits, scores, done=None, done_token=0, nsel=None, out=None
     if logits.dim() != 3:
         raise ValueError(f"logits: {logits.dim()} dimensions, need [batch][beams][vocab]")
     batch, beams, vocab = logits.shape
-    if vocab > 1 and logits.stride(2) != 1:
+    s0, s1, s2 = logits.stride()
+    if vocab > 1 and s2 != 1:
         raise ValueError("logits: a row must be contiguous")
-    row = logits.stride(1) if beams > 1 else (logits.stride(0) if batch > 1 else vocab)
-    if beams > 1 and batch > 1 and logits.stride(0) != beams * row:
+    row = s1 if beams > 1 else (s0 if batch > 1 else vocab)
+    if beams > 1 and batch > 1 and s0 != beams * row:
         raise ValueError("logits: rows must be evenly spaced")
     nsel = beams if nsel is None else int(nsel)
     dev = logits.device
@@ -510,46 +550,40 @@ def ssq_beam_select(logits, scores, done=None, done_token=0, nsel=None, out=None
                torch.empty((batch, nsel), dtype=torch.int32, device=dev))
     score, parent, token = out
     _on(dev, scores=scores, done=done, score=score, parent=parent, token=token)
-    with torch.cuda.device(dev):
+    with _Launch(dev, stream) as st:
         _check(_lib.ssq_beam_select(
             batch, beams, vocab, _ACT_TYPES[logits.dtype], logits.data_ptr(), row,
             _ptr(scores, "scores", torch.float32, batch * beams),
             _ptr(done, "done", torch.uint8, batch * beams, allow_none=True), int(done_token), nsel,
             _ptr(score, "score", torch.float32, batch * nsel),
             _ptr(parent, "parent", torch.int32, batch * nsel),
-            _ptr(token, "token", torch.int32, batch * nsel), _stream(stream)))
+            _ptr(token, "token", torch.int32, batch * nsel), st))
     return out
 
 
-def _beam_shape(parent):
+def _reorder(call, cfg, pool, slot_idx, parent, layer0, nl, stream):
     if not isinstance(parent, torch.Tensor) or parent.dim() != 2:
         raise ValueError("parent: expected an int32 tensor [batch][beams]")
-    return parent.shape
+    batch, beams = parent.shape
+    dev = parent.device
+    pp = _ptr(pool, "pool", torch.uint8, _pool_bytes(cfg))
+    parp = _ptr(parent, "parent", torch.int32, batch * beams)
+    _on(dev, pool=pool, slot_idx=slot_idx)
+    with _Launch(dev, stream) as st:
+        _check(call(cfg.ref, pp, _slots(slot_idx, batch * beams), batch, beams, parp, layer0, nl,
+                    st))
 
 
 def ssq_pool_reorder(cfg: Config, pool, slot_idx, parent, layer0, nl, stream=None):
     """In place, for nl layers: the slot of beam k of request r takes the
     state of the slot of its beam parent[r][k] (int32 [batch][beams]; -1
     leaves it as it is).  slot_idx int32 [batch][beams] or None."""
-    batch, beams = _beam_shape(parent)
-    pp = _pool_ptr(cfg, pool)
-    _on(parent.device, pool=pool, slot_idx=slot_idx)
-    with torch.cuda.device(parent.device):
-        _check(_lib.ssq_pool_reorder(cfg.ref, pp, _slots(slot_idx, batch * beams), batch, beams,
-                                     _ptr(parent, "parent", torch.int32, batch * beams), layer0,
-                                     nl, _stream(stream)))
+    _reorder(_lib.ssq_pool_reorder, cfg, pool, slot_idx, parent, layer0, nl, stream)
 
 
 def ssq_damp_pool_reorder(cfg: DampConfig, pool, slot_idx, parent, layer0, nl, stream=None):
     """ssq_pool_reorder for a DAMP pool."""
-    batch, beams = _beam_shape(parent)
-    L = ssq_damp_pool_layout(cfg)
-    pp = _ptr(pool, "pool", torch.uint8, L["pool_bytes"])
-    _on(parent.device, pool=pool, slot_idx=slot_idx)
-    with torch.cuda.device(parent.device):
-        _check(_lib.ssq_damp_pool_reorder(
-            cfg.ref, pp, _slots(slot_idx, batch * beams), batch, beams,
-            _ptr(parent, "parent", torch.int32, batch * beams), layer0, nl, _stream(stream)))
+    _reorder(_lib.ssq_damp_pool_reorder, cfg, pool, slot_idx, parent, layer0, nl, stream)
 
 
 def ssq_status_string(status) -> str:
