@@ -77,6 +77,7 @@ struct Tail {
     uint64_t cb_full[kRingCB], cb_empty[kRingCB], x_full[kRingX], x_empty[kRingX];
     uint64_t xs_ready[2], ds_full[2], m_ready[2], y_full[2], g_full, g_free, b_ready, drained[3];
     uint32_t tmem;
+    int item, dead;     // the block's item; a wait gave up
     int pos[2];         // region positions of the units' heads
 };
 constexpr int kSmemBytes = kOffTail + (int)sizeof(Tail);
@@ -705,16 +706,29 @@ chunk_kernel(const __grid_constant__ PoolView pv, const __grid_constant__ Ragged
     Tail& tl = *reinterpret_cast<Tail*>(sm + kOffTail);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
-    // ---- the block's work: pairs of units fastest, then requests, then segments
     const int tiles = (pv.P + kPT - 1) / kPT;
     const int per_group = pv.hpg * tiles, pairs_group = (per_group + 1) / 2;
     const int pairs = pairs_group * pv.G;
+    const int halves = pv.N > 64 ? 2 : 1;           // 64-column halves of C and B
+    if (tid == 0) tl.dead = 0;
+    if (warp == kElemWarps + 1) tc::alloc(&tl.tmem, kTmemCols);
+    const long long items = (long long)__ldcg(&rc.plan->count) * pairs;
+
+    // ---- one item after another: a pair of units of one segment of one run,
+    // handed out in order so that blocks that finish early take more
+    for (bool armed = false;;) {
+    if (tid == 0) tl.item = atomicAdd(&rc.plan->next[STATE ? 0 : 1], 1);
+    tc::fence_before();
+    __syncthreads();
+    tc::fence_after();
+    if (tl.item >= items || tl.dead) break;
+    const uint32_t tmem = tl.tmem;
     Work wk;
     {
-        const int pr = blockIdx.x % pairs;
-        const int rest = blockIdx.x / pairs;
-        wk.b = rest % rc.batch;
-        wk.seg = rest / rc.batch;
+        const int entry = tl.item / pairs, pr = tl.item - entry * pairs;
+        const int2 at = __ldcg(&rc.plan->entry[entry]);
+        wk.b = at.x;
+        wk.seg = at.y;
         wk.g = pr / pairs_group;
         const int u0 = (pr - wk.g * pairs_group) * 2;
         wk.nu = min(2, per_group - u0);
@@ -725,17 +739,21 @@ chunk_kernel(const __grid_constant__ PoolView pv, const __grid_constant__ Ragged
             wk.p0[u] = uu % tiles * kPT;
         }
     }
-    wk.run = ragged_run(pv, rc, wk.b, false);       // the token kernel reports
-    if (!wk.run.ok || wk.run.len < rc.chunk_min) return;
+    wk.run = ragged_run(pv, rc, wk.b, false);       // (the token kernel reports)
     const int chunks = (wk.run.len + kL - 1) / kL;
-    wk.nseg = rc.nseg > 1 ? (chunks + rc.seg_chunks - 1) / rc.seg_chunks : 1;
-    wk.c0 = rc.nseg > 1 ? wk.seg * rc.seg_chunks : 0;
-    wk.nc = rc.nseg > 1 ? min(rc.seg_chunks, chunks - wk.c0) : chunks;
-    if (wk.seg >= wk.nseg || (STATE && wk.seg + 1 >= wk.nseg)) return;
+    wk.nseg = run_segments(rc, wk.run.len);
+    wk.c0 = wk.seg * rc.seg_chunks;
+    wk.nc = min(rc.seg_chunks, chunks - wk.c0);
     const int nu = wk.nu, nc = wk.nc;
+    if (STATE && wk.seg + 1 >= wk.nseg) {           // the last segment's state is not needed
+        __syncthreads();
+        continue;
+    }
 
     // ---- set-up ----
     if (tid == 0) {
+        if (armed)
+            for (uint64_t* m = tl.cb_full; m < tl.drained + 3; ++m) mbar_inval(m);
         for (int i = 0; i < kRingCB; ++i) {
             mbar_init(&tl.cb_full[i], 1);
             mbar_init(&tl.cb_empty[i], STATE ? nu : nu + 1);
@@ -760,12 +778,8 @@ chunk_kernel(const __grid_constant__ PoolView pv, const __grid_constant__ Ragged
 #pragma unroll
         for (int u = 0; u < 2; ++u)
             if (pv.perm[i] == wk.h[u]) tl.pos[u] = i;
-    if (warp == kElemWarps + 1) tc::alloc(&tl.tmem, kTmemCols);
-    tc::fence_before();
     __syncthreads();
-    tc::fence_after();
-    const uint32_t tmem = tl.tmem;
-    const int halves = pv.N > 64 ? 2 : 1;           // 64-column halves of C and B
+    armed = true;
     bool ok = true;
 
     // the parts of w X that the stored state can show: fp32 rows take three
@@ -895,11 +909,12 @@ chunk_kernel(const __grid_constant__ PoolView pv, const __grid_constant__ Ragged
         }
         __syncwarp();
     }
-    if (!ok) atomicOr(reinterpret_cast<unsigned*>(pv.pool), SSQ_DEVERR_TIMEOUT);
-    tc::fence_before();
-    __syncthreads();
-    tc::fence_after();
-    if (warp == kElemWarps + 1) tc::dealloc(tmem, kTmemCols);
+    if (!ok) {
+        tl.dead = 1;
+        atomicOr(reinterpret_cast<unsigned*>(pv.pool), SSQ_DEVERR_TIMEOUT);
+    }
+    }
+    if (warp == kElemWarps + 1) tc::dealloc(tl.tmem, kTmemCols);
 }
 
 // ---------------------------------------------------------------------------
@@ -919,7 +934,7 @@ chunk_join(const __grid_constant__ PoolView pv, const __grid_constant__ RaggedCa
     const int pos = unit / tiles, h = pv.perm[pos];
     const Run run = ragged_run(pv, rc, b, false);
     if (!run.ok || run.len < rc.chunk_min) return;
-    const int nseg = ((run.len + kL - 1) / kL + rc.seg_chunks - 1) / rc.seg_chunks;
+    const int nseg = run_segments(rc, run.len);
     if (nseg < 2) return;
     const int j = threadIdx.x % LPR, p = unit % tiles * kRows + threadIdx.x / LPR;
     const bool active = p < pv.P;
@@ -1024,19 +1039,20 @@ cudaError_t launch_pass(const PoolView& pv, const RaggedCall& rc, const ChunkMap
     thread_local int done = -1;
     cudaError_t e = allow_smem(chunk_kernel<STATE>, kSmemBytes, &done);
     if (e != cudaSuccess) return e;
-    const long long blocks = (long long)chunk_pairs(pv.H, pv.P, pv.G) * rc.batch * rc.nseg;
-    if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-    chunk_kernel<STATE><<<(unsigned)blocks, kCThreadsTotal, kSmemBytes, st>>>(pv, rc, maps, fmt);
+    const long long items = (long long)chunk_pairs(pv.H, pv.P, pv.G) * rc.batch * rc.nseg;
+    if (items > 0x3fffffffLL) return cudaErrorInvalidConfiguration;
+    const unsigned blocks = (unsigned)(items < kSMs ? items : kSMs);
+    chunk_kernel<STATE><<<blocks, kCThreadsTotal, kSmemBytes, st>>>(pv, rc, maps, fmt);
     return cudaGetLastError();
 }
 
 }  // namespace
 
-void chunk_plan(int H, int P, int N, int G, int batch, int max_len, int* nseg, int* seg_chunks)
+void chunk_plan(int H, int P, int G, int batch, int max_len, int* nseg, int* seg_chunks)
 {
     *nseg = 1;
-    *seg_chunks = 1;
-    if (N > 128 || batch < 1) return;
+    *seg_chunks = 0x7fffffff / kL;                  // a run is one segment
+    if (batch < 1) return;
     const int chunks = (int)(((long long)max_len + kL - 1) / kL);
     const long long blocks = (long long)chunk_pairs(H, P, G) * batch;
     const long long fit = kSMs / blocks;

@@ -15,6 +15,7 @@
 
 #include "ssq_ragged.h"
 #include "ssq_rowio.cuh"
+#include "ssq_serve_params.h"
 
 namespace ssq {
 
@@ -43,14 +44,178 @@ __device__ __forceinline__ void store_act(void* p, long long i, float v)
         reinterpret_cast<float*>(p)[i] = v;
 }
 
+// E consecutive activations as fp32 pairs, in pieces as wide as the address
+// allows.
+template <int TYPE, int E>
+__device__ __forceinline__ void load_acts(const void* p, long long i, float2 (&v)[E / 2])
+{
+    constexpr int EB = TYPE == SSQ_T_F32 ? 4 : 2, PER = 16 / EB;
+    const char* a = reinterpret_cast<const char*>(p) + i * EB;
+    if ((reinterpret_cast<uintptr_t>(a) & 15) == 0) {
+#pragma unroll
+        for (int k = 0; k < E / PER; ++k) {
+            const uint4 w = __ldg(reinterpret_cast<const uint4*>(a) + k);
+            const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+            if constexpr (TYPE == SSQ_T_F32) {
+                v[2 * k] = make_float2(__uint_as_float(u[0]), __uint_as_float(u[1]));
+                v[2 * k + 1] = make_float2(__uint_as_float(u[2]), __uint_as_float(u[3]));
+            } else {
+#pragma unroll
+                for (int m = 0; m < 4; ++m) {
+                    if constexpr (TYPE == SSQ_T_BF16)
+                        v[4 * k + m] = make_float2(__uint_as_float(u[m] << 16),
+                                                   __uint_as_float(u[m] & 0xffff0000u));
+                    else
+                        v[4 * k + m] = __half22float2(*reinterpret_cast<const __half2*>(&u[m]));
+                }
+            }
+        }
+    } else {
+#pragma unroll
+        for (int k = 0; k < E; k += 2)
+            v[k / 2] = make_float2(load_act<TYPE>(p, i + k), load_act<TYPE>(p, i + k + 1));
+    }
+}
+
 // Floats of one staged row of B or C: LPR pieces of E floats, 4 floats apart.
 template <int N>
 constexpr int kRowF = Shape<N>::LPR * (Shape<N>::E + 4);
 
-template <int FMT, int N, int TYPE>
-__global__ void __launch_bounds__(kThreads)
-tokens_kernel(const __grid_constant__ PoolView pv, const __grid_constant__ RaggedCall rc)
+// ---- single tokens --------------------------------------------------------
+// One warp takes `steps` groups of RPW = 32/LPR rows of one head of one request
+// and loads a group's rows while it works on the one before.  No shared memory, no barrier: what bounds it
+// is the pool's traffic (fp rows) or the issue of the refit and rounding
+// (integer rows).
+template <int RF, int N, int TYPE>
+__device__ __forceinline__ void single_unit(const PoolView& pv, const RaggedCall& rc,
+                                            const Run& run, const RowPlace& place, int h, int p0,
+                                            int steps)
 {
+    constexpr int E = Shape<N>::E, LPR = Shape<N>::LPR, RPW = Shape<N>::RPW;
+    const int lane = threadIdx.x & 31, j = lane % LPR;
+    const int g = h / pv.hpg;
+    const long long t = run.t0;
+    int p = p0 + lane / LPR;
+    RawRow<RF, N> next;
+    next.load(place, p, j, p < pv.P && !run.fresh);
+    const long long xat = t * rc.xs + (long long)h * pv.P;
+    float xn = p < pv.P ? load_act<TYPE>(rc.x, xat + p) : 0.0f;
+    const float dt = __ldg(rc.dt + t * rc.dts + h);
+    const long long Bat = t * rc.Bs + (long long)g * N + j * E;
+    const long long Cat = t * rc.Cs + (long long)g * N + j * E;
+    const float lam = decay(dt, __ldg(rc.A + h)), D = __ldg(rc.D + h);
+    const float2 l2 = make_float2(lam, lam);
+    for (int k = 0; k < steps; ++k) {
+        float s[E];
+        next.decode(s);
+        const float x = xn;
+        const int pn = p + RPW;
+        if (k + 1 < steps) {
+            next.load(place, pn, j, pn < pv.P && !run.fresh);
+            xn = pn < pv.P ? load_act<TYPE>(rc.x, xat + pn) : 0.0f;
+        }
+        const float dtx = __fmul_rn(dt, x);
+        const float2 x2 = make_float2(dtx, dtx);
+        float2 acc = make_float2(0.0f, 0.0f);
+#pragma unroll
+        for (int q = 0; q < E; q += 16) {            // B and C again from L1
+            float2 Bv[8], Cv[8];
+            load_acts<TYPE, 16>(rc.B, Bat + q, Bv);
+            load_acts<TYPE, 16>(rc.C, Cat + q, Cv);
+#pragma unroll
+            for (int n = 0; n < 16; n += 2) {
+                const float2 v = fma2(l2, make_float2(s[q + n], s[q + n + 1]), mul2(x2, Bv[n / 2]));
+                s[q + n] = v.x;
+                s[q + n + 1] = v.y;
+                acc = fma2(Cv[n / 2], v, acc);
+            }
+        }
+        const float y = grp_sum<LPR>(__fadd_rn(acc.x, acc.y));
+        if (p < pv.P && j == 0)
+            store_act<TYPE>(rc.y, t * rc.ys + (long long)h * pv.P + p, __fmaf_rn(D, x, y));
+        row_store<RF, N, true>(place, p, j, p < pv.P, s, reinterpret_cast<uint32_t*>(pv.pool));
+        p = pn;
+    }
+}
+
+template <int FMT, int N, int TYPE>
+__device__ __forceinline__ void single_tokens(const PoolView& pv, const RaggedCall& rc, int steps,
+                                              int blocks)
+{
+    const int rows = steps * Shape<N>::RPW;
+    const int tiles = (pv.P + rows - 1) / rows;
+    const int per = tiles * pv.H;
+    const long long units = (long long)per * rc.batch;
+    const int warps = blockDim.x / 32;
+    for (long long i = (long long)blockIdx.x * warps + threadIdx.x / 32; i < units;
+         i += (long long)blocks * warps) {
+        const int b = (int)(i / per), unit = (int)(i - (long long)b * per);
+        const int pos = unit / tiles, h = pv.perm[pos];
+        const Run run = ragged_run(pv, rc, b, unit == 0 && threadIdx.x % 32 == 0);
+        if (!run.ok || run.len != 1) continue;
+        const RowPlace place = place_head<FMT>(pv, run.slot, rc.layer, pos);
+        const int p0 = unit % tiles * rows;
+        const int n = min(steps, (pv.P - p0 + Shape<N>::RPW - 1) / Shape<N>::RPW);
+        if constexpr (Fmt<FMT>::quant) {
+            if (!place.quant) {
+                single_unit<SSQ_F32, N, TYPE>(pv, rc, run, place, h, p0, n);
+                continue;
+            }
+        }
+        single_unit<FMT, N, TYPE>(pv, rc, run, place, h, p0, n);
+    }
+}
+
+// The chunk kernel's work list, in the order of the requests: one block.
+__device__ __forceinline__ void write_plan(const PoolView& pv, const RaggedCall& rc)
+{
+    __shared__ int warp_sum[kThreads / 32];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid / 32, warps = blockDim.x / 32;
+    int base = 0;
+    for (int b0 = 0; b0 < rc.batch; b0 += blockDim.x) {
+        const int b = b0 + tid;
+        int n = 0;
+        if (b < rc.batch) {
+            const Run run = ragged_run(pv, rc, b, false);
+            if (run.ok && run.len >= rc.chunk_min) n = run_segments(rc, run.len);
+        }
+        int upto = n;                                // of this warp's requests
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, upto, o);
+            if (lane >= o) upto += v;
+        }
+        if (lane == 31) warp_sum[warp] = upto;
+        __syncthreads();
+        int at = base + upto - n;
+        for (int w = 0; w < warps; ++w) {
+            if (w < warp) at += warp_sum[w];
+            base += warp_sum[w];
+        }
+        for (int k = 0; k < n; ++k) rc.plan->entry[at + k] = make_int2(b, k);
+        __syncthreads();
+    }
+    if (tid == 0) {
+        rc.plan->count = base;
+        rc.plan->next[0] = 0;
+        rc.plan->next[1] = 0;
+    }
+}
+
+template <int FMT, int N, int TYPE>
+__global__ void __launch_bounds__(kThreads, 2)
+tokens_kernel(const __grid_constant__ PoolView pv, const __grid_constant__ RaggedCall rc,
+              int steps, int single_blocks)
+{
+    if ((int)blockIdx.x < single_blocks) {
+        single_tokens<FMT, N, TYPE>(pv, rc, steps, single_blocks);
+        return;
+    }
+    int block = (int)blockIdx.x - single_blocks;
+    if (rc.plan && --block < 0) {
+        write_plan(pv, rc);
+        return;
+    }
     constexpr int E = Shape<N>::E, LPR = Shape<N>::LPR;
     __shared__ __align__(16) float sB[kTok][kRowF<N>], sC[kTok][kRowF<N>];
     __shared__ float sLam[kTok], sDt[kTok];
@@ -58,14 +223,14 @@ tokens_kernel(const __grid_constant__ PoolView pv, const __grid_constant__ Ragge
     const int rows = blockDim.x / LPR;
     const int tiles = (pv.P + rows - 1) / rows;
     const int per = tiles * pv.H;
-    const int b = blockIdx.x / per;
-    const int unit = blockIdx.x - b * per;
+    const int b = block / per;
+    const int unit = block - b * per;
     const int tile = unit % tiles;
     const int pos = unit / tiles;                  // region position of the head
     const int h = pv.perm[pos];
     const int tid = threadIdx.x;
-    const Run run = ragged_run(pv, rc, b, unit == 0 && tid == 0);
-    if (!run.ok || run.len >= rc.chunk_min) return;
+    const Run run = ragged_run(pv, rc, b, false);
+    if (!run.ok || run.len >= rc.chunk_min || run.len == 1) return;
     if (run.len == 0 && !run.fresh) return;
 
     const int j = tid % LPR;
@@ -130,17 +295,34 @@ template <int FMT, int N>
 cudaError_t launch_n(const PoolView& pv, const RaggedCall& rc, cudaStream_t st)
 {
     constexpr int LPR = Shape<N>::LPR;
-    // whole warps that cover the head's rows, at most kThreads
+    // Single tokens: warps of up to 8 groups of rows each, on a grid that is
+    // resident at once (two blocks per SM).
+    constexpr int kWarps = kThreads / 32;
+    const long long resident = 2LL * kSMs;
+    const long long groups = (long long)((pv.P + Shape<N>::RPW - 1) / Shape<N>::RPW) * pv.H
+                             * rc.batch;
+    int steps = 8;
+    while (steps > 1 && groups < resident * kWarps * steps) steps /= 2;
+    const int rows1 = steps * Shape<N>::RPW;
+    const long long units = (long long)((pv.P + rows1 - 1) / rows1) * pv.H * rc.batch;
+    long long single = (units + kWarps - 1) / kWarps;
+    if (single > resident) single = resident;
+    // Runs of several tokens: blocks of whole warps over a head's rows.  Runs
+    // of no token (a fresh slot is zeroed) go with them.
     int threads = (pv.P * LPR + 31) / 32 * 32;
     if (threads > kThreads) threads = kThreads;
     const int rows = threads / LPR;
     const long long blocks = (long long)((pv.P + rows - 1) / rows) * pv.H * rc.batch;
-    if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-    const unsigned grid = (unsigned)blocks;
+    if (blocks + single > 0x7ffffff0LL) return cudaErrorInvalidConfiguration;
+    const unsigned grid = (unsigned)(single + (rc.plan ? 1 : 0) + blocks);
+    const int sb = (int)single;
     switch (rc.type) {
-    case SSQ_T_BF16: tokens_kernel<FMT, N, SSQ_T_BF16><<<grid, threads, 0, st>>>(pv, rc); break;
-    case SSQ_T_F16: tokens_kernel<FMT, N, SSQ_T_F16><<<grid, threads, 0, st>>>(pv, rc); break;
-    default: tokens_kernel<FMT, N, SSQ_T_F32><<<grid, threads, 0, st>>>(pv, rc); break;
+    case SSQ_T_BF16:
+        tokens_kernel<FMT, N, SSQ_T_BF16><<<grid, threads, 0, st>>>(pv, rc, steps, sb); break;
+    case SSQ_T_F16:
+        tokens_kernel<FMT, N, SSQ_T_F16><<<grid, threads, 0, st>>>(pv, rc, steps, sb); break;
+    default:
+        tokens_kernel<FMT, N, SSQ_T_F32><<<grid, threads, 0, st>>>(pv, rc, steps, sb); break;
     }
     return cudaGetLastError();
 }

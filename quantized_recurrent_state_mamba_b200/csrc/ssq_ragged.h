@@ -6,6 +6,14 @@
 
 namespace ssq {
 
+// What the chunk kernel's passes work through, written by the token kernel
+// before them: the (request, segment) entries of the runs that go through
+// chunks, and per pass the next item to hand out.
+struct ChunkPlan {
+    int count, next[2], pad;
+    int2 entry[1];                   // batch * nseg places
+};
+
 struct RaggedCall {
     const int32_t* slot_idx;   // [batch] or null (identity)
     const int32_t* cu;         // [batch+1]
@@ -21,6 +29,7 @@ struct RaggedCall {
     // chunk kernel: segments of seg_chunks chunks; states [batch][nseg][H][P][N]
     // and decays [batch][nseg][H] of the workspace (nseg > 1)
     int nseg, seg_chunks;
+    ChunkPlan* plan;                 // null: no run goes through chunks
     float* ws_state;
     float* ws_decay;
 };
@@ -51,6 +60,13 @@ __device__ __forceinline__ Run ragged_run(const PoolView& pv, const RaggedCall& 
     return r;
 }
 
+// Segments of a run in chunks of 128 tokens.
+__device__ __forceinline__ int run_segments(const RaggedCall& rc, int len)
+{
+    const int chunks = (len + 127) / 128;
+    return rc.nseg > 1 ? (chunks + rc.seg_chunks - 1) / rc.seg_chunks : 1;
+}
+
 // Token by token (ssq_ragged.cu), and in chunks on the tensor cores
 // (ssq_chunk.cu).
 cudaError_t launch_ragged_tokens(const PoolView& pv, const RaggedCall& rc, int fmt,
@@ -58,6 +74,6 @@ cudaError_t launch_ragged_tokens(const PoolView& pv, const RaggedCall& rc, int f
 cudaError_t launch_ragged_chunks(const PoolView& pv, const RaggedCall& rc, int fmt,
                                  cudaStream_t st);
 // Segments that the longest run is cut into, and their length in chunks.
-void chunk_plan(int H, int P, int N, int G, int batch, int max_len, int* nseg, int* seg_chunks);
+void chunk_plan(int H, int P, int G, int batch, int max_len, int* nseg, int* seg_chunks);
 
 }  // namespace ssq

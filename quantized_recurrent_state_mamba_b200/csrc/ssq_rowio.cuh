@@ -32,63 +32,81 @@ __device__ __forceinline__ RowPlace place_head(const PoolView& pv, int slot, int
     return rp;
 }
 
-// Entries [j*E, j*E+E) of row p as fp32.  Every lane of the warp calls this
-// with the same head; lanes that are not `active` get zeros and read nothing.
-template <int FMT, int N>
-__device__ __forceinline__ void row_load(const RowPlace& rp, int p, int j, bool active,
-                                         float (&s)[Shape<N>::E])
-{
-    using F = Fmt<FMT>;
-    constexpr int E = Shape<N>::E;
-    if constexpr (F::quant) {
-        if (rp.quant) {
-            constexpr int CB = E * F::bits / 8;
-            Chunk<CB> c;
+// A lane's part of a row as it is stored, RF the format of the row (fp rows of
+// the integer formats are SSQ_F32): loaded at one point, decoded at another.
+template <int RF, int N>
+struct RawRow {
+    using F = Fmt<RF>;
+    static constexpr int E = Shape<N>::E;
+    static constexpr int CB = E * F::bits / 8;
+    Chunk<CB> c;
+    float delta, z;
+
+    // Lanes that are not `active` get a zero row and read nothing.
+    __device__ __forceinline__ void load(const RowPlace& rp, int p, int j, bool active)
+    {
 #pragma unroll
-            for (int i = 0; i < CB / 4; ++i) c.w[i] = 0;
-            float delta = 0.0f, z = 0.0f;
-            if (active) {
-                load_chunk<CB>(c, rp.codes + (long long)p * (N * F::bits / 8) + j * CB);
-                if constexpr (F::sym) {
-                    delta = reinterpret_cast<const float*>(rp.meta)[p];
-                } else {
-                    const float2 m = reinterpret_cast<const float2*>(rp.meta)[p];
-                    delta = m.x;
-                    z = m.y;
-                }
+        for (int i = 0; i < CB / 4; ++i) c.w[i] = 0;
+        delta = 0.0f;
+        z = 0.0f;
+        if (!active) return;
+        const uint8_t* rows = F::quant ? rp.codes : rp.fp;
+        load_chunk<CB>(c, rows + (long long)p * (N * F::bits / 8) + j * CB);
+        if constexpr (F::quant) {
+            if constexpr (F::sym) {
+                delta = __ldcs(reinterpret_cast<const float*>(rp.meta) + p);
+            } else {
+                const float2 m = __ldcs(reinterpret_cast<const float2*>(rp.meta) + p);
+                delta = m.x;
+                z = m.y;
             }
-            decode_row<FMT, E>(c, delta, z, s);
-            return;
         }
     }
-#pragma unroll
-    for (int n = 0; n < E; ++n) s[n] = 0.0f;
-    if (active) {
-        if constexpr (FMT == SSQ_BF16) {
-            Chunk<E * 2> c;
-            load_chunk<E * 2>(c, rp.fp + ((long long)p * N + j * E) * 2);
+    // Every lane of the warp calls this.
+    __device__ __forceinline__ void decode(float (&s)[E]) const
+    {
+        if constexpr (F::quant) {
+            decode_row<RF, E>(c, delta, z, s);
+        } else if constexpr (RF == SSQ_BF16) {
 #pragma unroll
             for (int n = 0; n < E; ++n)
                 s[n] = __uint_as_float((c.w[n / 2] >> (16 * (n % 2))) << 16);
         } else {
-            Chunk<E * 4> c;
-            load_chunk<E * 4>(c, rp.fp + ((long long)p * N + j * E) * 4);
 #pragma unroll
             for (int n = 0; n < E; ++n) s[n] = __uint_as_float(c.w[n]);
         }
     }
+};
+
+// Entries [j*E, j*E+E) of row p as fp32.  Every lane of the warp calls this
+// with the same head.
+template <int FMT, int N>
+__device__ __forceinline__ void row_load(const RowPlace& rp, int p, int j, bool active,
+                                         float (&s)[Shape<N>::E])
+{
+    if constexpr (Fmt<FMT>::quant) {
+        if (!rp.quant) {
+            RawRow<SSQ_F32, N> f;
+            f.load(rp, p, j, active);
+            f.decode(s);
+            return;
+        }
+    }
+    RawRow<FMT, N> r;
+    r.load(rp, p, j, active);
+    r.decode(s);
 }
 
 // Refit, round and store row p (fp rows: convert and store).  Every lane of
 // the warp calls this; lanes that are not `active` store nothing.
-template <int FMT, int N>
+template <int FMT, int N, bool ALL_QUANT = false>
 __device__ __forceinline__ void row_store(const RowPlace& rp, int p, int j, bool active,
                                           const float (&s)[Shape<N>::E], uint32_t* err)
 {
     using F = Fmt<FMT>;
     constexpr int E = Shape<N>::E, LPR = Shape<N>::LPR;
     if constexpr (F::quant) {
-        if (rp.quant) {
+        if (ALL_QUANT || rp.quant) {
             constexpr int CB = E * F::bits / 8;
             RowParams q = refit_row<FMT, E, LPR>(s);
             // min and max pass over NaN entries; a sum of zeros does not

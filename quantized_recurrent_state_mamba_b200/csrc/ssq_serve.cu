@@ -58,24 +58,42 @@ ssq_status check_reorder(int n_layers, int n_slots, const int32_t* slot_idx, int
     return batch > 0 ? need(parent, "parent", 4) : SSQ_OK;
 }
 
-// The workspace of a call whose runs are cut into nseg segments: a state and
-// a decay per request, segment and head.
-size_t segment_state_bytes(const ssq_config* cfg, int batch, int nseg)
+// Whether the shape can go through chunks at all.
+bool chunks_shape(const ssq_config* cfg, int max_len)
 {
-    return (size_t)batch * nseg * cfg->nheads * cfg->headdim * cfg->d_state * 4;
+    return max_len >= kChunkMin && cfg->headdim % 8 == 0 && cfg->d_state <= 128;
 }
-size_t segment_decay_bytes(const ssq_config* cfg, int batch, int nseg)
+// ... and the call: bf16, whole 16-byte pieces.
+bool chunks_fit(const ssq_config* cfg, int max_len, const ssq_tokens* t)
 {
-    return (size_t)batch * nseg * cfg->nheads * 4;
-}
-
-// Whether the chunk kernel takes the call: bf16, whole 16-byte pieces.
-bool chunks_fit(const ssq_config* cfg, const ssq_tokens* t)
-{
-    return t->type == SSQ_T_BF16 && cfg->headdim % 8 == 0 && cfg->d_state <= 128 && t->total > 0
+    return chunks_shape(cfg, max_len) && t->type == SSQ_T_BF16 && t->total > 0
            && t->x_stride % 8 == 0 && t->B_stride % 8 == 0 && t->C_stride % 8 == 0
            && t->y_stride % 8 == 0 && aligned(t->x, 16) && aligned(t->B, 16)
            && aligned(t->C, 16) && aligned(t->y, 16);
+}
+
+// The workspace of runs that go through chunks: the work list, and where the
+// longest is cut into nseg > 1 segments a state and a decay per request,
+// segment and head.  Offsets in bytes.
+struct Workspace {
+    int nseg, seg_chunks;
+    size_t state, decay, total;
+};
+Workspace workspace_of(const ssq_config* cfg, int batch, int max_len)
+{
+    Workspace w;
+    memset(&w, 0, sizeof(w));
+    if (batch < 1 || !chunks_shape(cfg, max_len)) return w;
+    ssq::chunk_plan(cfg->nheads, cfg->headdim, cfg->ngroups, batch, max_len, &w.nseg,
+                    &w.seg_chunks);
+    const size_t places = (size_t)batch * w.nseg;
+    w.state = (sizeof(ssq::ChunkPlan) + places * sizeof(int2) + 255) / 256 * 256;
+    w.decay = w.total = w.state;
+    if (w.nseg > 1) {
+        w.decay += places * cfg->nheads * cfg->headdim * cfg->d_state * 4;
+        w.total = w.decay + places * cfg->nheads * 4;
+    }
+    return w;
 }
 
 ssq_status run_reorder(const ssq::ReorderCall& rc, cudaStream_t stream)
@@ -98,11 +116,7 @@ ssq_status ssq_prefill_ragged_workspace(const ssq_config* cfg, int batch, int ma
     if (batch < 0) return fail(SSQ_ERR_INVALID_ARG, "batch %d < 0", batch);
     if (max_len < 0) return fail(SSQ_ERR_INVALID_ARG, "max_len %d < 0", max_len);
     if (!bytes) return fail(SSQ_ERR_INVALID_ARG, "bytes is NULL");
-    int nseg = 1, seg_chunks = 1;
-    ssq::chunk_plan(cfg->nheads, cfg->headdim, cfg->d_state, cfg->ngroups, batch, max_len, &nseg,
-                    &seg_chunks);
-    *bytes = nseg > 1 ? segment_state_bytes(cfg, batch, nseg) + segment_decay_bytes(cfg, batch, nseg)
-                      : 0;
+    *bytes = workspace_of(cfg, batch, max_len).total;
     return SSQ_OK;
 }
 
@@ -139,13 +153,12 @@ ssq_status ssq_prefill_ragged(const ssq_config* cfg, void* pool, const int32_t* 
     }
     SSQ_TRY(need(A, "A", 4));
     SSQ_TRY(need(D, "D", 4));
-    size_t want = 0;
-    SSQ_TRY(ssq_prefill_ragged_workspace(cfg, batch, max_len, &want));
-    if (want > 0) {
+    const Workspace ws = workspace_of(cfg, batch, max_len);
+    if (ws.total > 0) {
         SSQ_TRY(need(workspace, "workspace", 256));
-        if (workspace_bytes < want)
+        if (workspace_bytes < ws.total)
             return fail(SSQ_ERR_INVALID_ARG, "workspace of %zu bytes, need %zu", workspace_bytes,
-                        want);
+                        ws.total);
     }
     if (batch == 0) return SSQ_OK;
     ssq::RaggedCall rc;
@@ -171,15 +184,15 @@ ssq_status ssq_prefill_ragged(const ssq_config* cfg, void* pool, const int32_t* 
     rc.Cs = tok->C_stride;
     rc.dts = tok->dt_stride;
     rc.ys = tok->y_stride;
-    const bool chunked = max_len >= kChunkMin && chunks_fit(cfg, tok);
+    const bool chunked = chunks_fit(cfg, max_len, tok);
     if (chunked) {
+        char* base = static_cast<char*>(workspace);
         rc.chunk_min = kChunkMin;
-        ssq::chunk_plan(cfg->nheads, cfg->headdim, cfg->d_state, cfg->ngroups, batch, max_len,
-                        &rc.nseg, &rc.seg_chunks);
-        if (rc.nseg > 1) {
-            rc.ws_state = static_cast<float*>(workspace);
-            rc.ws_decay = rc.ws_state + segment_state_bytes(cfg, batch, rc.nseg) / 4;
-        }
+        rc.nseg = ws.nseg;
+        rc.seg_chunks = ws.seg_chunks;
+        rc.plan = reinterpret_cast<ssq::ChunkPlan*>(base);
+        rc.ws_state = reinterpret_cast<float*>(base + ws.state);
+        rc.ws_decay = reinterpret_cast<float*>(base + ws.decay);
     }
     cudaError_t e = ssq::launch_ragged_tokens(pv, rc, (int)cfg->fmt, stream);
     if (e == cudaSuccess && chunked) e = ssq::launch_ragged_chunks(pv, rc, (int)cfg->fmt, stream);

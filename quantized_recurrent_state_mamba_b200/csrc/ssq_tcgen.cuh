@@ -10,6 +10,13 @@
 #include "ssq_pipe.cuh"
 
 namespace ssq {
+
+// The barrier's memory may be initialised again.
+__device__ __forceinline__ void mbar_inval(uint64_t* b)
+{
+    asm volatile("mbarrier.inval.shared::cta.b64 [%0];" :: "r"(saddr(b)) : "memory");
+}
+
 namespace tc {
 
 __device__ __forceinline__ void alloc(uint32_t* dst, unsigned ncols)
