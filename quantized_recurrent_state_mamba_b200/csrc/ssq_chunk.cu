@@ -19,7 +19,7 @@
 //                            inputs to 16 or 24 bits; TMEM
 //   Y1      [128 i x  64 p]  M (bf16, written to TMEM) times X; the columns of
 //                            dS, which has been read by then
-// The running sums are kept per block of 32 tokens: with r_i the sum from the
+// The running sums (in units of log 2) are kept per block of 32 tokens: with r_i the sum from the
 // start of i's block and q_j the sum behind j in its block, the decay between
 // two blocks is exp(r_i) * exp(sum of the blocks between) * exp(q_j), every
 // factor at most 1 for A <= 0, so only the diagonal blocks take an exp per
@@ -53,30 +53,51 @@ constexpr int kWg = 256;                // threads that work on a unit
 constexpr int kCThreadsTotal = 2 * kWg + 128;
 constexpr int kElemWarps = 2 * kWg / 32;
 constexpr float kLog2e = 1.4426950408889634f;
-// exp(-1000) is 0 in fp32: sums of clamped steps stay finite for A = -inf
-constexpr float kStepFloor = -1000.0f;
+// 2^-1500 is 0 in fp32: sums of clamped steps stay finite for A = -inf
+constexpr float kStepFloor = -1500.0f;
 
 // Shared memory, from its 1024-byte aligned start (the swizzle's period).
 constexpr int kTileCB = kL * 256;       // C or B: two halves of [128][64] bf16
 constexpr int kTileX = kL * 128;        // [128][64] bf16
-constexpr int kRingCB = 3, kRingX = 3;
-constexpr int kOffX = kRingCB * kTileCB;
-constexpr int kOffXs = kOffX + kRingX * kTileX;      // up to three bf16 parts of w X
-constexpr int kOffS = kOffXs + 3 * kTileX;           // states in bf16, one per unit
-constexpr int kOffTail = kOffS + 2 * kTileX;
+// Places of the rings: C and B take turns in three; the first pass over
+// segments loads no C and keeps no state operand, so it has a ring of two for
+// B, one more place for x, and a buffer of w X for each unit.
+template <bool STATE>
+struct Mem {
+    static constexpr int ring_cb = STATE ? 2 : 3, ring_x = STATE ? 4 : 3;
+    static constexpr int x = ring_cb * kTileCB;
+    static constexpr int xs = x + ring_x * kTileX;   // up to three bf16 parts of w X
+    static constexpr int xs_unit = STATE ? 3 * kTileX : 0;
+    static constexpr int s = xs + 3 * kTileX;        // states in bf16, one per unit
+};
+constexpr int kOffTail = Mem<false>::s + 2 * kTileX;
+static_assert(Mem<true>::xs + 6 * kTileX <= kOffTail, "the passes share one size");
+constexpr int kMaxRing = 4;
 
 struct UnitArrays {
     float f[kL];        // dt_j exp(q_j)
-    float r2[kL];       // r_j log2(e) - log2(dt_j)
+    float nr[kL];       // log2(dt_j) - r_j
     float block[4];     // sums of the four blocks
     int bad[kPT];       // first token of the chunk with a non-finite x in row p
-    int any_bad, pad[3];
+    int any_bad;
+    float decay;        // of the segment so far (first pass)
+    float A2, D;        // A log2(e) and D of the unit's head
+};
+// What a block works on.
+struct Work {
+    Run run;
+    int b, seg, nseg;        // request, segment, segments of the run
+    int c0, nc;              // chunks of the segment
+    int h[2], p0[2], nu;     // units
+    int g;
 };
 struct Tail {
     UnitArrays unit[2];
-    uint64_t cb_full[kRingCB], cb_empty[kRingCB], x_full[kRingX], x_empty[kRingX];
+    uint64_t cb_full[kMaxRing], cb_empty[kMaxRing], x_full[kMaxRing], x_empty[kMaxRing];
     uint64_t xs_ready[2], ds_full[2], m_ready[2], y_full[2], g_full, g_free, b_ready, drained[3];
     uint32_t tmem;
+    Work work;
+    int parts;          // of w X in a whole chunk
     int item, dead;     // the block's item; a wait gave up
     int pos[2];         // region positions of the units' heads
 };
@@ -103,6 +124,22 @@ __device__ __forceinline__ float ex2(float x)
     float r;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
+}
+__device__ __forceinline__ float lg2(float x)
+{
+    float r;
+    asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+// A load that stays where it is written, ahead of its use (the compiler moved
+// a plain one down to the use, where a chunk waited for it); 0 unless `pred`.
+__device__ __forceinline__ float load_early(const float* p, bool pred)
+{
+    float v;
+    asm volatile("{\n .reg .pred p;\n setp.ne.u32 p, %2, 0;\n mov.f32 %0, 0f00000000;\n"
+                 " @p ld.global.nc.f32 %0, [%1];\n}\n"
+                 : "=f"(v) : "l"(p), "r"((unsigned)pred));
+    return v;
 }
 // {lo, hi} rounded to bf16 in one word
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
@@ -145,11 +182,7 @@ __device__ __noinline__ void pool_to_stage(const PoolView& pv, int slot, int lay
         const int r = r0 + t / LPR;
         float s[E];
         row_load<FMT, N>(place, p0 + r, j, r < kPT && p0 + r < pv.P, s);
-        if (r < kPT)
-#pragma unroll
-            for (int n = 0; n < E; n += 4)
-                *reinterpret_cast<float4*>(stage + r * N + j * E + n) =
-                    make_float4(s[n], s[n + 1], s[n + 2], s[n + 3]);
+        if (r < kPT) row_to_stage<FMT, N>(place, s, j, stage + r * N);
     }
 }
 template <int FMT, int N>
@@ -161,13 +194,8 @@ __device__ __noinline__ void stage_to_pool(const PoolView& pv, int slot, int lay
     const int j = t % LPR;
     for (int r0 = 0; r0 < kPT; r0 += kWg / LPR) {
         const int r = r0 + t / LPR;
-        const int rr = r < kPT ? r : 0;
         float s[E];
-#pragma unroll
-        for (int n = 0; n < E; n += 4) {
-            const float4 v = *reinterpret_cast<const float4*>(stage + rr * N + j * E + n);
-            s[n] = v.x; s[n + 1] = v.y; s[n + 2] = v.z; s[n + 3] = v.w;
-        }
+        row_from_stage<FMT, N>(place, s, j, stage + (r < kPT ? r : 0) * N);
         row_store<FMT, N>(place, p0 + r, j, r < kPT && p0 + r < pv.P, s,
                           reinterpret_cast<uint32_t*>(pv.pool));
     }
@@ -204,14 +232,6 @@ struct ChunkMaps {
     CUtensorMap x, B, C, y;
 };
 
-// What a block works on.
-struct Work {
-    Run run;
-    int b, seg, nseg;        // request, segment, segments of the run
-    int c0, nc;              // chunks of the segment
-    int h[2], p0[2], nu;     // units
-    int g;
-};
 
 // ---------------------------------------------------------------------------
 // Element work of unit u: 256 threads.  Thread (t, hf) is token t of the chunk
@@ -220,18 +240,13 @@ struct Work {
 // ---------------------------------------------------------------------------
 constexpr int kPH = kPT / 2;
 
-// bf16 pairs: products and sums rounded once
-__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b)
+__device__ __forceinline__ __nv_bfloat162 as_bf16x2(uint32_t w)
 {
-    uint32_t r;
-    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-    return r;
+    return *reinterpret_cast<__nv_bfloat162*>(&w);
 }
-__device__ __forceinline__ uint32_t fma_bf16x2(uint32_t a, uint32_t b, uint32_t c)
+__device__ __forceinline__ uint32_t as_word(__nv_bfloat162 v)
 {
-    uint32_t r;
-    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
-    return r;
+    return *reinterpret_cast<uint32_t*>(&v);
 }
 
 // Token t's part of w X as bf16 parts to shared memory.  Both return whether
@@ -241,42 +256,46 @@ __device__ __forceinline__ uint32_t fma_bf16x2(uint32_t a, uint32_t b, uint32_t 
 // the rest), hi = rn(x w1), e = x w1 - hi, which a fused multiply-add gives
 // exactly, and lo = rn(x w2 + e).  What is left out is 2^-17 of w and the
 // rounding of lo, 2^-9 of a term that is at most 2^-8 of the product.
-__device__ __forceinline__ bool weigh_x2(unsigned xrow, unsigned xs, int t, int hf, float wj)
+__device__ __forceinline__ bool weigh_x2(unsigned xrow, unsigned xs, unsigned at0,
+                                         float wj)
 {
-    const uint32_t w1 = pack_bf16(wj, wj);
-    const float rest = __fsub_rn(wj, unpack_bf16(w1).x);
-    const uint32_t w2 = pack_bf16(rest, rest);
-    uint32_t acc = 0;
+    const uint32_t w1w = pack_bf16(wj, wj);
+    const float rest = __fsub_rn(wj, unpack_bf16(w1w).x);
+    const __nv_bfloat162 w1 = as_bf16x2(w1w), w2 = as_bf16x2(pack_bf16(rest, rest));
+    const __nv_bfloat162 zero = as_bf16x2(0);
+    __nv_bfloat162 acc = zero;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const unsigned at = swz(t, 4 * hf + i);
+        const unsigned at = at0 ^ (16 * i);
         const uint4 xv = lds128(xrow + at);
         const uint32_t xw[4] = {xv.x, xv.y, xv.z, xv.w};
         uint32_t hi[4], lo[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-            acc = fma_bf16x2(xw[k], 0, acc);
-            hi[k] = mul_bf16x2(xw[k], w1);
-            lo[k] = fma_bf16x2(xw[k], w2, fma_bf16x2(xw[k], w1, hi[k] ^ 0x80008000u));
+            const __nv_bfloat162 x = as_bf16x2(xw[k]);
+            acc = __hfma2(x, zero, acc);
+            const __nv_bfloat162 h = __hmul2_rn(x, w1);
+            hi[k] = as_word(h);
+            lo[k] = as_word(__hfma2(x, w2, __hfma2(x, w1, __hneg2(h))));
         }
         sts128(xs + at, make_uint4(hi[0], hi[1], hi[2], hi[3]));
         sts128(xs + kTileX + at, make_uint4(lo[0], lo[1], lo[2], lo[3]));
     }
-    return (acc & 0x7fff7fffu) != 0;
+    return (as_word(acc) & 0x7fff7fffu) != 0;
 }
 
 // Three parts, in fp32: rn(w x), the rounding of the rest, and of the rest of
 // that.  Without FULL, tokens that are not `inside` the run become zero, in
 // x's buffer too.
 template <bool FULL, bool ZERO_X>
-__device__ __forceinline__ bool weigh_x3(unsigned xrow, unsigned xs, int t, int hf, float wj,
-                                         bool inside)
+__device__ __forceinline__ bool weigh_x3(unsigned xrow, unsigned xs, unsigned at0,
+                                         float wj, bool inside)
 {
     const float2 w2 = make_float2(wj, wj), zero2 = make_float2(0.0f, 0.0f);
     float2 acc = zero2;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const unsigned at = swz(t, 4 * hf + i);
+        const unsigned at = at0 ^ (16 * i);
         uint4 xv = lds128(xrow + at);
         if (!FULL && !inside) xv = make_uint4(0, 0, 0, 0);
         const uint32_t xw[4] = {xv.x, xv.y, xv.z, xv.w};
@@ -305,19 +324,28 @@ __device__ __forceinline__ bool weigh_x3(unsigned xrow, unsigned xs, int t, int 
     return !(acc.x + acc.y == 0.0f);
 }
 
+// The state's rows with a non-finite x become NaN.
+__device__ __forceinline__ void bad_state(const UnitArrays& ua, int hf, float (&S)[kPH])
+{
+#pragma unroll
+    for (int p = 0; p < kPH; ++p)
+        if (ua.bad[kPH * hf + p] < kL) S[p] = __int_as_float(0x7fffffff);
+}
+
 template <bool STATE>
 __device__ __forceinline__ bool unit_loop(const PoolView& pv, const RaggedCall& rc,
                                           const CUtensorMap* ymap, const Work& wk,
                                           unsigned char* sm, unsigned base, Tail& tl, uint32_t tmem, int u, int t,
-                                          int hf, int parts, float (&S)[kPH], float& decay_all)
+                                          int hf, float (&S)[kPH])
 {
     const int lane = t & 31, w = t >> 5;
-    const int h = wk.h[u], p0 = wk.p0[u], nu = wk.nu;
+    const int nu = wk.nu;
     UnitArrays& ua = tl.unit[u];
     const uint32_t tm = tmem + ((uint32_t)(w * 32) << 16);
-    const float A = __ldg(rc.A + h), D = __ldg(rc.D + h);
-    const unsigned s_op = base + kOffS + u * kTileX;
-    const unsigned xs = base + kOffXs;
+    using M = Mem<STATE>;
+    const unsigned s_op = base + M::s + u * kTileX;
+    const unsigned xs = base + M::xs + u * M::xs_unit;
+    const unsigned at0 = swz(t, 4 * hf);            // piece i of the thread's half line: at0 ^ 16 i
     bool ok = true;
     auto wait = [&](uint64_t* bar, unsigned parity) {
         if (ok) ok = tc::wait_phase(bar, parity);
@@ -326,7 +354,7 @@ __device__ __forceinline__ bool unit_loop(const PoolView& pv, const RaggedCall& 
     auto write_state = [&]() {   // S in bf16, line n of the operand
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-            sts128(s_op + swz(t, 4 * hf + i),
+            sts128(s_op + (at0 ^ (16 * i)),
                    make_uint4(pack_bf16(S[8 * i], S[8 * i + 1]), pack_bf16(S[8 * i + 2], S[8 * i + 3]),
                               pack_bf16(S[8 * i + 4], S[8 * i + 5]),
                               pack_bf16(S[8 * i + 6], S[8 * i + 7])));
@@ -343,131 +371,135 @@ __device__ __forceinline__ bool unit_loop(const PoolView& pv, const RaggedCall& 
     if (hf == 0 && t == 0) ua.any_bad = 0;
     const bool leader = hf == 0 && t == 0;          // issues the unit's stores
 
-    const long long tok0 = (long long)wk.run.t0 + (long long)wk.c0 * kL;
-    const int left0 = wk.run.len - wk.c0 * kL;      // tokens from the segment's start
-    auto load_dt = [&](int c) {
-        return c < wk.nc && c * kL + t < left0
-                   ? __ldg(rc.dt + (tok0 + (long long)c * kL + t) * rc.dts + h) : 0.0f;
+    const int tok0 = wk.run.t0 + wk.c0 * kL;        // the segment's first token
+    const int left0 = wk.run.len - wk.c0 * kL;      // tokens from there
+    auto dt_of = [&](int c) {
+        const int i = c * kL + t;
+        return load_early(rc.dt + (long long)(tok0 + i) * rc.dts + wk.h[u], i < left0);
     };
-    float dt = load_dt(0);
-    decay_all = 1.0f;
+    float dt = dt_of(0);
 
     for (int c = 0; c < wk.nc; ++c) {
         const int Lc = min(kL, left0 - c * kL);
-        const float dt_next = load_dt(c + 1);
-        // ---- running sums ----
-        float a = __fmul_rn(dt, A);
+        // ---- running sums: forward, and by one half backward ----
+        float a = __fmul_rn(dt, ua.A2);
         if (a < kStepFloor) a = kStepFloor;         // a NaN stays
         if (t >= Lc) a = 0.0f;                      // dt is 0 there, A may be infinite
-        float r = a, q = __shfl_down_sync(0xffffffffu, a, 1);
-        if (lane == 31) q = 0.0f;
+        float r = a;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const float v = __shfl_up_sync(0xffffffffu, r, o);
-            const float z = __shfl_down_sync(0xffffffffu, q, o);
             if (lane >= o) r += v;
-            if (lane + o < 32) q += z;
         }
-        const float f = __fmul_rn(dt, expf(q));
-        const float ri2 = __fmul_rn(r, kLog2e);
         if (hf == 0) {
-            ua.f[t] = f;
+            ua.nr[t] = __fsub_rn(lg2(dt), r);
             if (lane == 31) ua.block[w] = r;
         } else {
-            ua.r2[t] = __fsub_rn(ri2, __log2f(dt));
+            float q = __shfl_down_sync(0xffffffffu, a, 1);
+            if (lane == 31) q = 0.0f;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const float v = __shfl_down_sync(0xffffffffu, q, o);
+                if (lane + o < 32) q += v;
+            }
+            ua.f[t] = __fmul_rn(dt, ex2(q));
         }
+        dt = dt_of(c + 1);
         unit_sync(u);
-        const float4 bs = *reinterpret_cast<const float4*>(ua.block);
-        // sums of the blocks behind this one and of all; what lies between an
-        // earlier block and this one
-        float behind = 0.0f;
-        if (w < 3) behind = bs.w;
-        if (w < 2) behind += bs.z;
-        if (w < 1) behind += bs.y;
-        const float b2 = w == 3 ? bs.z : 0.0f;                 // between block 1 and this
-        const float b1 = w == 3 ? bs.y + bs.z : w == 2 ? bs.y : 0.0f;   // ... block 0 ...
-        const float before = (w > 0 ? bs.x : 0.0f) + (w > 1 ? (w == 2 ? bs.y : bs.y + bs.z) : 0.0f);
-        if (!STATE && leader && c > 0) {
-            // y of the chunk before has been read from its x buffer
-            bulk_wait_read<0>();
-            mbar_arrive(&tl.x_empty[((c - 1) * nu + u) % kRingX]);
+        // the sums of the chunk's blocks, read again where they are needed
+        // (registers are short here)
+        const float4& bs = *reinterpret_cast<const float4*>(ua.block);
+        float wj;
+        {
+            float behind = 0.0f;
+            if (w < 3) behind = bs.w;
+            if (w < 2) behind += bs.z;
+            if (w < 1) behind += bs.y;
+            wj = __fmul_rn(ua.f[t], ex2(behind));
         }
-        __syncwarp();
-        const float wj = __fmul_rn(f, expf(behind));
-        const float lam = expf((bs.x + bs.y) + (bs.z + bs.w));
-        decay_all = __fmul_rn(decay_all, lam);
 
         // ---- w X in parts ----
-        const int kx = c * nu + u, xslot = kx % kRingX;
-        const unsigned xrow = base + kOffX + xslot * kTileX;
-        wait(&tl.x_full[xslot], (kx / kRingX) & 1);
-        // the other unit's product has read the shared buffer
-        if (u == 0) {
-            if (c > 0) wait(&tl.ds_full[nu - 1], (c - 1) & 1);
-        } else {
-            wait(&tl.ds_full[0], c & 1);
+        const int kx = c * nu + u, xslot = kx % M::ring_x;
+        const unsigned xrow = base + M::x + xslot * kTileX;
+        wait(&tl.x_full[xslot], (kx / M::ring_x) & 1);
+        if constexpr (STATE) {
+            if (c > 0) wait(&tl.ds_full[u], (c - 1) & 1);       // (seen before: at once)
+        } else if (nu > 1) {
+            // the other unit's product has read the shared buffer
+            if (u == 1)
+                wait(&tl.ds_full[0], c & 1);
+            else if (c > 0)
+                wait(&tl.ds_full[1], (c - 1) & 1);
         }
-        const bool bad = Lc < kL ? weigh_x3<false, !STATE>(xrow, xs, t, hf, wj, t < Lc)
-                         : parts == 2 ? weigh_x2(xrow, xs, t, hf, wj)
-                                      : weigh_x3<true, !STATE>(xrow, xs, t, hf, wj, true);
+        const bool bad = Lc < kL ? weigh_x3<false, !STATE>(xrow, xs, at0, wj, t < Lc)
+                         : tl.parts == 2 ? weigh_x2(xrow, xs, at0, wj)
+                                      : weigh_x3<true, !STATE>(xrow, xs, at0, wj, true);
         if (bad) {
             // rare: take the non-finite entries of this token out
             ua.any_bad = 1;
             for (int p = kPH * hf; p < kPH * hf + kPH; ++p) {
-                const unsigned at = swz(t, p >> 3) + (p & 7) * 2;
+                const unsigned pa = swz(t, p >> 3) + (p & 7) * 2;
                 unsigned short v;
-                asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(xrow + at) : "memory");
+                asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(xrow + pa) : "memory");
                 if ((v & 0x7f80u) == 0x7f80u) {
                     atomicMin(&ua.bad[p], t);
                     const unsigned short z = 0;
-                    asm volatile("st.shared.u16 [%0], %1;" :: "r"(xrow + at), "h"(z) : "memory");
-                    for (int k = 0; k < 3; ++k)
+                    asm volatile("st.shared.u16 [%0], %1;" :: "r"(xrow + pa), "h"(z) : "memory");
+                    for (int k = 0; k < (Lc < kL ? 3 : tl.parts); ++k)
                         asm volatile("st.shared.u16 [%0], %1;"
-                                     :: "r"(xs + k * kTileX + at), "h"(z) : "memory");
+                                     :: "r"(xs + k * kTileX + pa), "h"(z) : "memory");
                 }
             }
         }
         __syncwarp();
         fence_proxy_async();
         mbar_arrive(&tl.xs_ready[u]);
+        if (!STATE && leader && c > 0) {
+            // y of the chunk before has been read from its x buffer
+            bulk_wait_read<0>();
+            mbar_arrive(&tl.x_empty[((c - 1) * nu + u) % M::ring_x]);
+        }
 
         // ---- M ----
         if constexpr (!STATE) {
+            // what lies between an earlier block and this one
+            const float b2 = w == 3 ? bs.z : 0.0f;
+            const float b1 = w == 3 ? bs.y + bs.z : w == 2 ? bs.y : 0.0f;
             wait(&tl.g_full, c & 1);
             tc::fence_after();
             for (int k = 0; k < w; ++k) {           // blocks before the diagonal one
                 const int j0 = 32 * k + 16 * hf;
                 float gv[16];
                 tc::ld16(tm + kColG + j0, gv);
-                const float uk = expf(r + (k == 0 ? b1 : k == 1 ? b2 : 0.0f));
+                const float uk = ex2(r + (k == 0 ? b1 : k == 1 ? b2 : 0.0f));
                 const float2 u2 = make_float2(uk, uk);
-                float2 cf[8];
-#pragma unroll
-                for (int m = 0; m < 4; ++m) {
-                    const float4 fv = *reinterpret_cast<const float4*>(&ua.f[j0 + 4 * m]);
-                    cf[2 * m] = mul2(make_float2(fv.x, fv.y), u2);
-                    cf[2 * m + 1] = mul2(make_float2(fv.z, fv.w), u2);
-                }
                 tc::wait_ld(gv);
                 uint32_t mw[8];
 #pragma unroll
-                for (int m = 0; m < 8; ++m) {
-                    const float2 v = mul2(make_float2(gv[2 * m], gv[2 * m + 1]), cf[m]);
-                    mw[m] = pack_bf16(v.x, v.y);
+                for (int m = 0; m < 4; ++m) {
+                    const float4 fv = *reinterpret_cast<const float4*>(&ua.f[j0 + 4 * m]);
+                    const float2 v0 = mul2(make_float2(gv[4 * m], gv[4 * m + 1]),
+                                           mul2(make_float2(fv.x, fv.y), u2));
+                    const float2 v1 = mul2(make_float2(gv[4 * m + 2], gv[4 * m + 3]),
+                                           mul2(make_float2(fv.z, fv.w), u2));
+                    mw[2 * m] = pack_bf16(v0.x, v0.y);
+                    mw[2 * m + 1] = pack_bf16(v1.x, v1.y);
                 }
                 tc::st8(tm + col_m(u) + j0 / 2, mw);
             }
             {
                 const int j0 = 32 * w + 16 * hf;
-                float gv[16], cf[16];
+                const float2 r2 = make_float2(r, r);
+                float gv[16];
                 tc::ld16(tm + kColG + j0, gv);
+                float2 cf[8];
 #pragma unroll
-                for (int m = 0; m < 16; m += 4) {
-                    const float4 rv = *reinterpret_cast<const float4*>(&ua.r2[j0 + m]);
-                    cf[m] = ex2(__fsub_rn(ri2, rv.x));
-                    cf[m + 1] = ex2(__fsub_rn(ri2, rv.y));
-                    cf[m + 2] = ex2(__fsub_rn(ri2, rv.z));
-                    cf[m + 3] = ex2(__fsub_rn(ri2, rv.w));
+                for (int m = 0; m < 4; ++m) {
+                    const float4 nv = *reinterpret_cast<const float4*>(&ua.nr[j0 + 4 * m]);
+                    const float2 e0 = add2(r2, make_float2(nv.x, nv.y));
+                    const float2 e1 = add2(r2, make_float2(nv.z, nv.w));
+                    cf[2 * m] = make_float2(ex2(e0.x), ex2(e0.y));
+                    cf[2 * m + 1] = make_float2(ex2(e1.x), ex2(e1.y));
                 }
                 tc::wait_ld(gv);
                 tc::fence_before();
@@ -475,11 +507,10 @@ __device__ __forceinline__ bool unit_loop(const PoolView& pv, const RaggedCall& 
                 uint32_t mw[8];
                 const int li = lane - 16 * hf;      // columns up to li are at or before i
 #pragma unroll
-                for (int m = 0; m < 16; m += 2) {
+                for (int m = 0; m < 8; ++m) {
                     // j > i: 0 whatever G holds there
-                    const float v0 = m <= li ? __fmul_rn(gv[m], cf[m]) : 0.0f;
-                    const float v1 = m + 1 <= li ? __fmul_rn(gv[m + 1], cf[m + 1]) : 0.0f;
-                    mw[m / 2] = pack_bf16(v0, v1);
+                    const float2 v = mul2(make_float2(gv[2 * m], gv[2 * m + 1]), cf[m]);
+                    mw[m] = pack_bf16(2 * m <= li ? v.x : 0.0f, 2 * m + 1 <= li ? v.y : 0.0f);
                 }
                 tc::st8(tm + col_m(u) + j0 / 2, mw);
             }
@@ -487,77 +518,92 @@ __device__ __forceinline__ bool unit_loop(const PoolView& pv, const RaggedCall& 
         }
 
         // ---- state ----
-        wait(&tl.xs_ready[u], c & 1);               // every thread's any_bad is seen
-        const bool any_bad = ua.any_bad != 0;
         wait(&tl.ds_full[u], c & 1);
         tc::fence_after();
         {
+            const float lam = ex2((bs.x + bs.y) + (bs.z + bs.w));
+            if (STATE && leader) ua.decay = __fmul_rn(ua.decay, lam);
             const float2 l2 = make_float2(lam, lam);
-            float d[2][16];
-            tc::ld16(tm + col_y1(u) + kPH * hf, d[0]);
-            tc::ld16(tm + col_y1(u) + kPH * hf + 16, d[1]);
-            tc::wait_ld(d[0]);
-            tc::after_wait(d[1]);
 #pragma unroll
-            for (int m = 0; m < kPH; m += 2) {
-                const float2 v = fma2(l2, make_float2(S[m], S[m + 1]),
-                                      make_float2(d[m / 16][m % 16], d[m / 16][m % 16 + 1]));
-                S[m] = v.x;
-                S[m + 1] = v.y;
+            for (int k = 0; k < kPH; k += 16) {
+                float d[16];
+                tc::ld16(tm + col_y1(u) + kPH * hf + k, d);
+                tc::wait_ld(d);
+                if (k + 16 == kPH) {
+                    tc::fence_before();
+                    if constexpr (!STATE) mbar_arrive(&tl.m_ready[u]);
+                }
+#pragma unroll
+                for (int m = 0; m < 16; m += 2) {
+                    const float2 v = fma2(l2, make_float2(S[k + m], S[k + m + 1]),
+                                          make_float2(d[m], d[m + 1]));
+                    S[k + m] = v.x;
+                    S[k + m + 1] = v.y;
+                }
             }
         }
-        tc::fence_before();
-        if (any_bad) {
-#pragma unroll
-            for (int p = 0; p < kPH; ++p)
-                if (ua.bad[kPH * hf + p] < kL) S[p] = __int_as_float(0x7fffffff);
-        }
-        if constexpr (!STATE) {
-            mbar_arrive(&tl.m_ready[u]);
-
+        if constexpr (STATE) {
+            unit_sync(u);                           // the x buffer has been read by all
+            if (leader) mbar_arrive(&tl.x_empty[xslot]);
+            if (ua.any_bad) {
+                bad_state(ua, hf, S);
+                unit_sync(u);
+                if (hf == 0 && t < kPT) ua.bad[t] = kL;
+                if (leader) ua.any_bad = 0;
+                unit_sync(u);
+            }
+        } else {
             // ---- y ----
-            const float ei = expf(r + before);
-            const float2 e2 = make_float2(ei, ei), D2 = make_float2(D, D);
+            const float before = (w > 0 ? bs.x : 0.0f) + (w > 1 ? bs.y : 0.0f)
+                                 + (w > 2 ? bs.z : 0.0f);
+            const float ei = ex2(r + before);
+            const float2 e2 = make_float2(ei, ei), D2 = make_float2(ua.D, ua.D);
             wait(&tl.y_full[u], c & 1);
             tc::fence_after();
             if (c + 1 < wk.nc) write_state();       // Y2 of this chunk has read the old one
 #pragma unroll
-            for (int k = 0; k < kPH; k += 16) {
+            for (int k = 0; k < kPH; k += 8) {
                 const int p = kPH * hf + k;
-                float y1[16], y2[16];
-                tc::ld16(tm + col_y1(u) + p, y1);
-                tc::ld16(tm + col_y2(u) + p, y2);
-                const unsigned a0 = xrow + swz(t, p / 8), a1 = xrow + swz(t, p / 8 + 1);
-                const uint4 xa = lds128(a0), xb = lds128(a1);
-                tc::wait_ld(y1);
-                tc::after_wait(y2);
-                const uint32_t xw[8] = {xa.x, xa.y, xa.z, xa.w, xb.x, xb.y, xb.z, xb.w};
-                float2 v[8];
+                float y1[8], y2[8];
+                tc::ld8(tm + col_y1(u) + p, y1);
+                tc::ld8(tm + col_y2(u) + p, y2);
+                const unsigned xa = xrow + (at0 ^ (2 * k));
+                const uint4 xv = lds128(xa);
+                tc::wait_ld8(y1, y2);
+                const uint32_t xw[4] = {xv.x, xv.y, xv.z, xv.w};
+                uint32_t yw[4];
 #pragma unroll
-                for (int m = 0; m < 8; ++m) {
-                    v[m] = fma2(e2, make_float2(y2[2 * m], y2[2 * m + 1]),
-                                make_float2(y1[2 * m], y1[2 * m + 1]));
-                    v[m] = fma2(D2, unpack_bf16(xw[m]), v[m]);
+                for (int m = 0; m < 4; ++m) {
+                    float2 v = fma2(e2, make_float2(y2[2 * m], y2[2 * m + 1]),
+                                    make_float2(y1[2 * m], y1[2 * m + 1]));
+                    v = fma2(D2, unpack_bf16(xw[m]), v);
+                    yw[m] = pack_bf16(v.x, v.y);
                 }
-                if (any_bad) {
-#pragma unroll
-                    for (int m = 0; m < 8; ++m) {
-                        if (ua.bad[p + 2 * m] <= t) v[m].x = __int_as_float(0x7fffffff);
-                        if (ua.bad[p + 2 * m + 1] <= t) v[m].y = __int_as_float(0x7fffffff);
-                    }
-                }
-                sts128(a0, make_uint4(pack_bf16(v[0].x, v[0].y), pack_bf16(v[1].x, v[1].y),
-                                      pack_bf16(v[2].x, v[2].y), pack_bf16(v[3].x, v[3].y)));
-                sts128(a1, make_uint4(pack_bf16(v[4].x, v[4].y), pack_bf16(v[5].x, v[5].y),
-                                      pack_bf16(v[6].x, v[6].y), pack_bf16(v[7].x, v[7].y)));
+                sts128(xa, make_uint4(yw[0], yw[1], yw[2], yw[3]));
             }
             tc::fence_before();
             fence_proxy_async();
             unit_sync(u);
-            const int tok = (int)tok0 + c * kL;
+            if (ua.any_bad) {
+                // rare: NaN for the rows with a non-finite x, from its token on
+                bad_state(ua, hf, S);
+                if (c + 1 < wk.nc) write_state();
+                for (int p = kPH * hf; p < kPH * hf + kPH; ++p)
+                    if (ua.bad[p] <= t) {
+                        const unsigned short nan = 0x7fff;
+                        asm volatile("st.shared.u16 [%0], %1;"
+                                     :: "r"(xrow + swz(t, p >> 3) + (p & 7) * 2), "h"(nan) : "memory");
+                    }
+                fence_proxy_async();
+                unit_sync(u);
+                if (hf == 0 && t < kPT) ua.bad[t] = kL;
+                if (leader) ua.any_bad = 0;
+                unit_sync(u);
+            }
+            const int tok = tok0 + c * kL, p0 = wk.p0[u], h = wk.h[u];
             if (Lc == kL) {
                 if (leader && ok) {
-                    tc::tma_store3(ymap, sm + kOffX + xslot * kTileX, p0, h, tok);
+                    tc::tma_store3(ymap, sm + M::x + xslot * kTileX, p0, h, tok);
                     bulk_commit();
                 }
             } else if (ok) {
@@ -570,15 +616,7 @@ __device__ __forceinline__ bool unit_loop(const PoolView& pv, const RaggedCall& 
                         *reinterpret_cast<uint4*>(yp + (long long)row * rc.ys) =
                             lds128(xrow + swz(row, ch));
             }
-        } else {
-            unit_sync(u);                           // the x buffer and `bad` have been read
-            if (leader) mbar_arrive(&tl.x_empty[xslot]);
         }
-        if (any_bad && hf == 0 && t < kPT) {
-            ua.bad[t] = kL;
-            ua.any_bad = 0;
-        }
-        dt = dt_next;
     }
     if (!STATE && leader) bulk_wait_read<0>();      // the buffers outlive the stores
     __syncwarp();
@@ -590,14 +628,14 @@ __device__ __forceinline__ bool unit_loop(const PoolView& pv, const RaggedCall& 
 // address is a function of the chunk counter alone.
 // ---------------------------------------------------------------------------
 template <bool STATE>
-__device__ __forceinline__ int slot_b(int c) { return (STATE ? c : 2 * c + 1) % kRingCB; }
+__device__ __forceinline__ int slot_b(int c) { return (STATE ? c : 2 * c + 1) % Mem<STATE>::ring_cb; }
 template <bool STATE>
 __device__ __forceinline__ unsigned phase_b(int c)
 {
-    return (unsigned)((STATE ? c : 2 * c + 1) / kRingCB) & 1u;
+    return (unsigned)((STATE ? c : 2 * c + 1) / Mem<STATE>::ring_cb) & 1u;
 }
-__device__ __forceinline__ int slot_c(int c) { return 2 * c % kRingCB; }
-__device__ __forceinline__ unsigned phase_c(int c) { return (unsigned)(2 * c / kRingCB) & 1u; }
+__device__ __forceinline__ int slot_c(int c) { return 2 * c % Mem<false>::ring_cb; }
+__device__ __forceinline__ unsigned phase_c(int c) { return (unsigned)(2 * c / Mem<false>::ring_cb) & 1u; }
 
 // G = C B^T of every chunk.
 __device__ __forceinline__ bool issue_g(unsigned base, Tail& tl, uint32_t tmem, int nc,
@@ -644,7 +682,8 @@ __device__ __forceinline__ bool issue_unit(unsigned base, Tail& tl, uint32_t tme
 {
     constexpr uint32_t kShapeY = tc::shape(128, 64, false, true);
     constexpr uint32_t kShapeS = tc::shape(128, 64, true, true);
-    const unsigned xs = base + kOffXs, so = base + kOffS + U * kTileX;
+    using M = Mem<STATE>;
+    const unsigned xs = base + M::xs + U * M::xs_unit, so = base + M::s + U * kTileX;
     for (int c = 0; c < nc; ++c) {
         const unsigned sb = base + slot_b<STATE>(c) * kTileCB;
         bool ok = STATE ? tc::wait_phase(&tl.cb_full[slot_b<STATE>(c)], phase_b<STATE>(c))
@@ -682,7 +721,7 @@ __device__ __forceinline__ bool issue_unit(unsigned base, Tail& tl, uint32_t tme
             if (tc::elect()) {
                 tc::fence_after();
                 const uint64_t dx =
-                    tc::operand(base + kOffX + ((c * nu + U) % kRingX) * kTileX);
+                    tc::operand(base + M::x + ((c * nu + U) % M::ring_x) * kTileX);
 #pragma unroll
                 for (int k = 0; k < kL / 16; ++k)
                     tc::mma_ta(tmem + col_y1(U), tmem + col_m(U) + k * 8, dx + k * 128, kShapeY,
@@ -700,6 +739,7 @@ __global__ void __launch_bounds__(kCThreadsTotal, 1)
 chunk_kernel(const __grid_constant__ PoolView pv, const __grid_constant__ RaggedCall rc,
              const __grid_constant__ ChunkMaps maps, int fmt)
 {
+    using M = Mem<STATE>;
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     unsigned char* sm = smem_raw;
     const unsigned base = saddr(sm);
@@ -723,8 +763,8 @@ chunk_kernel(const __grid_constant__ PoolView pv, const __grid_constant__ Ragged
     tc::fence_after();
     if (tl.item >= items || tl.dead) break;
     const uint32_t tmem = tl.tmem;
-    Work wk;
-    {
+    Work& wk = tl.work;
+    if (tid == 0) {
         const int entry = tl.item / pairs, pr = tl.item - entry * pairs;
         const int2 at = __ldcg(&rc.plan->entry[entry]);
         wk.b = at.x;
@@ -738,13 +778,19 @@ chunk_kernel(const __grid_constant__ PoolView pv, const __grid_constant__ Ragged
             wk.h[u] = wk.g * pv.hpg + uu / tiles;
             wk.p0[u] = uu % tiles * kPT;
         }
+        wk.run = ragged_run(pv, rc, wk.b, false);   // (the token kernel reports)
+        const int chunks = (wk.run.len + kL - 1) / kL;
+        wk.nseg = run_segments(rc, wk.run.len);
+        wk.c0 = wk.seg * rc.seg_chunks;
+        wk.nc = min(rc.seg_chunks, chunks - wk.c0);
     }
-    wk.run = ragged_run(pv, rc, wk.b, false);       // (the token kernel reports)
-    const int chunks = (wk.run.len + kL - 1) / kL;
-    wk.nseg = run_segments(rc, wk.run.len);
-    wk.c0 = wk.seg * rc.seg_chunks;
-    wk.nc = min(rc.seg_chunks, chunks - wk.c0);
+    __syncthreads();
     const int nu = wk.nu, nc = wk.nc;
+    if (tid < 2) {
+        tl.unit[tid].A2 = __fmul_rn(__ldg(rc.A + wk.h[tid]), kLog2e);
+        tl.unit[tid].D = __ldg(rc.D + wk.h[tid]);
+        tl.unit[tid].decay = 1.0f;
+    }
     if (STATE && wk.seg + 1 >= wk.nseg) {           // the last segment's state is not needed
         __syncthreads();
         continue;
@@ -754,11 +800,9 @@ chunk_kernel(const __grid_constant__ PoolView pv, const __grid_constant__ Ragged
     if (tid == 0) {
         if (armed)
             for (uint64_t* m = tl.cb_full; m < tl.drained + 3; ++m) mbar_inval(m);
-        for (int i = 0; i < kRingCB; ++i) {
+        for (int i = 0; i < kMaxRing; ++i) {
             mbar_init(&tl.cb_full[i], 1);
             mbar_init(&tl.cb_empty[i], STATE ? nu : nu + 1);
-        }
-        for (int i = 0; i < kRingX; ++i) {
             mbar_init(&tl.x_full[i], 1);
             mbar_init(&tl.x_empty[i], 1);
         }
@@ -781,21 +825,20 @@ chunk_kernel(const __grid_constant__ PoolView pv, const __grid_constant__ Ragged
     __syncthreads();
     armed = true;
     bool ok = true;
-
     // the parts of w X that the stored state can show: fp32 rows take three
     // (24 bits), rows of 16 bits and less two (16 bits)
     int parts = 2;
     for (int u = 0; u < nu; ++u)
         if (fmt == SSQ_F32 || (fmt != SSQ_BF16 && tl.pos[u] >= pv.Hq)) parts = 3;
+    if (tid == 0) tl.parts = parts;
 
     if (warp < kElemWarps) {
         const int u = tid / kWg, t = tid & (kL - 1), hf = tid / kL & 1;
         const bool mine = u < nu;
         const int h = wk.h[u], p0 = wk.p0[u];
         float S[kPH];       // S[p]: row p0 + 32 hf + p, entry t
-        float decay_all = 1.0f;
         // staging of the states at the ends: w X's buffers and the bf16 states'
-        float* stage = reinterpret_cast<float*>(sm + (u == 0 ? kOffXs : kOffS));
+        float* stage = reinterpret_cast<float*>(sm + (u == 0 ? M::xs : M::s));
         const int ph = kPH * hf;
         const long long unit_state = ((long long)h * pv.P + p0 + ph) * pv.N + t;
         const long long seg_state = ((long long)wk.b * rc.nseg + wk.seg) * pv.H * pv.P * pv.N;
@@ -818,8 +861,7 @@ chunk_kernel(const __grid_constant__ PoolView pv, const __grid_constant__ Ragged
         }
         units_sync();       // the staging is read before the loops write there
         if (mine)
-            ok = unit_loop<STATE>(pv, rc, &maps.y, wk, sm, base, tl, tmem, u, t, hf, parts, S,
-                                  decay_all);
+            ok = unit_loop<STATE>(pv, rc, &maps.y, wk, sm, base, tl, tmem, u, t, hf, S);
         units_sync();       // the loops are done with the staging
         if (mine && ok) {
             if constexpr (STATE) {
@@ -828,7 +870,7 @@ chunk_kernel(const __grid_constant__ PoolView pv, const __grid_constant__ Ragged
                 for (int p = 0; p < kPH; ++p)
                     if (t < pv.N && p0 + ph + p < pv.P) dst[p * pv.N] = S[p];
                 if (t == 0 && hf == 0 && p0 == 0)
-                    rc.ws_decay[((long long)wk.b * rc.nseg + wk.seg) * pv.H + h] = decay_all;
+                    rc.ws_decay[((long long)wk.b * rc.nseg + wk.seg) * pv.H + h] = tl.unit[u].decay;
             } else if (wk.seg + 1 == wk.nseg) {
 #pragma unroll
                 for (int p = 0; p < kPH; ++p)
@@ -847,9 +889,9 @@ chunk_kernel(const __grid_constant__ PoolView pv, const __grid_constant__ Ragged
             const int tok0 = wk.run.t0 + wk.c0 * kL;
             int k = 0, kx = 0;
             auto load_cb = [&](const CUtensorMap* map, int tok) {
-                const int s = k % kRingCB;
-                if (k >= kRingCB && ok)
-                    ok = tc::wait_phase(&tl.cb_empty[s], (k / kRingCB - 1) & 1);
+                const int s = k % M::ring_cb;
+                if (k >= M::ring_cb && ok)
+                    ok = tc::wait_phase(&tl.cb_empty[s], (k / M::ring_cb - 1) & 1);
                 if (!ok) return;
                 mbar_arrive_tx(&tl.cb_full[s], (unsigned)(halves * kTileX));
                 for (int hf = 0; hf < halves; ++hf)
@@ -858,12 +900,12 @@ chunk_kernel(const __grid_constant__ PoolView pv, const __grid_constant__ Ragged
                 ++k;
             };
             auto load_x = [&](int u, int tok) {
-                const int s = kx % kRingX;
-                if (kx >= kRingX && ok)
-                    ok = tc::wait_phase(&tl.x_empty[s], (kx / kRingX - 1) & 1);
+                const int s = kx % M::ring_x;
+                if (kx >= M::ring_x && ok)
+                    ok = tc::wait_phase(&tl.x_empty[s], (kx / M::ring_x - 1) & 1);
                 if (!ok) return;
                 mbar_arrive_tx(&tl.x_full[s], kTileX);
-                tc::tma_load3(sm + kOffX + s * kTileX, &maps.x, wk.p0[u], wk.h[u], tok,
+                tc::tma_load3(sm + M::x + s * kTileX, &maps.x, wk.p0[u], wk.h[u], tok,
                               &tl.x_full[s]);
                 ++kx;
             };
@@ -884,10 +926,10 @@ chunk_kernel(const __grid_constant__ PoolView pv, const __grid_constant__ Ragged
                 if (nu > 1) load_x(1, tok);
             }
             // no copy is in flight when the block ends, whatever happened
-            for (int i = max(0, k - kRingCB); i < k; ++i)
-                tc::wait_phase(&tl.cb_full[i % kRingCB], (i / kRingCB) & 1);
-            for (int i = max(0, kx - kRingX); i < kx; ++i)
-                tc::wait_phase(&tl.x_full[i % kRingX], (i / kRingX) & 1);
+            for (int i = max(0, k - M::ring_cb); i < k; ++i)
+                tc::wait_phase(&tl.cb_full[i % M::ring_cb], (i / M::ring_cb) & 1);
+            for (int i = max(0, kx - M::ring_x); i < kx; ++i)
+                tc::wait_phase(&tl.x_full[i % M::ring_x], (i / M::ring_x) & 1);
         }
         __syncwarp();
     } else {
@@ -919,58 +961,82 @@ chunk_kernel(const __grid_constant__ PoolView pv, const __grid_constant__ Ragged
 
 // ---------------------------------------------------------------------------
 // Segments' starting states: S_0 from the pool (or zero), S_{k+1} = decay_k
-// S_k + state_k; S_k replaces state_k in the workspace.  The lanes of a row
-// hold E entries each, as in the pool.
+// S_k + state_k; S_k replaces state_k in the workspace.  A block takes
+// kJoinRows rows of a head: the stored rows go through shared memory into the
+// workspace's order, in which a thread owns kJoinVec float4 and loads those of
+// the next segment before it stores those of this one.
 // ---------------------------------------------------------------------------
+constexpr int kJoinThreads = 128;
+
 template <int FMT, int N>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kJoinThreads)
 chunk_join(const __grid_constant__ PoolView pv, const __grid_constant__ RaggedCall rc)
 {
     constexpr int E = Shape<N>::E, LPR = Shape<N>::LPR;
-    constexpr int kRows = kThreads / LPR;
+    constexpr int kRows = kJoinThreads / LPR;        // kRows*N = 128*E floats
+    constexpr int kVec = kRows * N / 4 / kJoinThreads;
+    __shared__ __align__(16) float stage[kRows * N];
     const int tiles = (pv.P + kRows - 1) / kRows;
     const int per = tiles * pv.H;
     const int b = blockIdx.x / per, unit = blockIdx.x - b * per;
-    const int pos = unit / tiles, h = pv.perm[pos];
+    const int pos = unit / tiles, h = pv.perm[pos], r0 = unit % tiles * kRows;
     const Run run = ragged_run(pv, rc, b, false);
     if (!run.ok || run.len < rc.chunk_min) return;
     const int nseg = run_segments(rc, run.len);
     if (nseg < 2) return;
-    const int j = threadIdx.x % LPR, p = unit % tiles * kRows + threadIdx.x / LPR;
-    const bool active = p < pv.P;
-    float s[E];
+    const int tid = threadIdx.x, j = tid % LPR, r = tid / LPR;
+    float4 s[kVec];
     if (run.fresh) {
 #pragma unroll
-        for (int n = 0; n < E; ++n) s[n] = 0.0f;
+        for (int k = 0; k < kVec; ++k) s[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     } else {
-        row_load<FMT, N>(place_head<FMT>(pv, run.slot, rc.layer, pos), p, j, active, s);
-    }
-    if (!active) return;
-    const long long seg_floats = (long long)pv.H * pv.P * N;
-    float* at = rc.ws_state + (long long)b * rc.nseg * seg_floats
-                + ((long long)h * pv.P + p) * N + j * E;
-    const float* dec = rc.ws_decay + (long long)b * rc.nseg * pv.H + h;
-    for (int k = 0; k < nseg; ++k, at += seg_floats, dec += pv.H) {
-        const float l = k + 1 < nseg ? *dec : 0.0f;
+        float v[E];
+        const RowPlace place = place_head<FMT>(pv, run.slot, rc.layer, pos);
+        row_load<FMT, N>(place, r0 + r, j, r0 + r < pv.P, v);
+        row_to_stage<FMT, N>(place, v, j, stage + r * N);
+        __syncthreads();
 #pragma unroll
-        for (int n = 0; n < E; n += 4) {
-            float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            if (k + 1 < nseg) v = *reinterpret_cast<const float4*>(at + n);
-            *reinterpret_cast<float4*>(at + n) = make_float4(s[n], s[n + 1], s[n + 2], s[n + 3]);
-            s[n] = __fmaf_rn(l, s[n], v.x);
-            s[n + 1] = __fmaf_rn(l, s[n + 1], v.y);
-            s[n + 2] = __fmaf_rn(l, s[n + 2], v.z);
-            s[n + 3] = __fmaf_rn(l, s[n + 3], v.w);
-        }
+        for (int k = 0; k < kVec; ++k)
+            s[k] = reinterpret_cast<const float4*>(stage)[k * kJoinThreads + tid];
+    }
+    // the rows of the tile that exist, in float4
+    const int live = min(kRows, pv.P - r0) * N / 4;
+    const long long seg_vecs = (long long)pv.H * pv.P * N / 4;
+    float4* at = reinterpret_cast<float4*>(rc.ws_state) + (long long)b * rc.nseg * seg_vecs
+                 + ((long long)h * pv.P + r0) * N / 4;
+    const float* dec = rc.ws_decay + (long long)b * rc.nseg * pv.H + h;
+    float4 next[kVec];
+#pragma unroll
+    for (int k = 0; k < kVec; ++k)
+        if (k * kJoinThreads + tid < live) next[k] = at[k * kJoinThreads + tid];
+    for (int q = 0; q < nseg; ++q, at += seg_vecs, dec += pv.H) {
+        const float l = q + 1 < nseg ? *dec : 0.0f;
+        float4 cur[kVec];
+#pragma unroll
+        for (int k = 0; k < kVec; ++k) cur[k] = next[k];
+        if (q + 2 < nseg)
+#pragma unroll
+            for (int k = 0; k < kVec; ++k)
+                if (k * kJoinThreads + tid < live) next[k] = at[seg_vecs + k * kJoinThreads + tid];
+#pragma unroll
+        for (int k = 0; k < kVec; ++k)
+            if (k * kJoinThreads + tid < live) {
+                at[k * kJoinThreads + tid] = s[k];
+                s[k].x = __fmaf_rn(l, s[k].x, cur[k].x);
+                s[k].y = __fmaf_rn(l, s[k].y, cur[k].y);
+                s[k].z = __fmaf_rn(l, s[k].z, cur[k].z);
+                s[k].w = __fmaf_rn(l, s[k].w, cur[k].w);
+            }
     }
 }
 
 template <int FMT, int N>
 cudaError_t join_n(const PoolView& pv, const RaggedCall& rc, cudaStream_t st)
 {
-    constexpr int kRows = kThreads / Shape<N>::LPR;
-    const unsigned grid = (unsigned)((pv.P + kRows - 1) / kRows * pv.H * rc.batch);
-    chunk_join<FMT, N><<<grid, kThreads, 0, st>>>(pv, rc);
+    constexpr int kRows = kJoinThreads / Shape<N>::LPR;
+    const long long grid = (long long)((pv.P + kRows - 1) / kRows) * pv.H * rc.batch;
+    if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+    chunk_join<FMT, N><<<(unsigned)grid, kJoinThreads, 0, st>>>(pv, rc);
     return cudaGetLastError();
 }
 template <int FMT>

@@ -49,26 +49,31 @@ __device__ __forceinline__ void store_act(void* p, long long i, float v)
 template <int TYPE, int E>
 __device__ __forceinline__ void load_acts(const void* p, long long i, float2 (&v)[E / 2])
 {
-    constexpr int EB = TYPE == SSQ_T_F32 ? 4 : 2, PER = 16 / EB;
+    constexpr int EB = TYPE == SSQ_T_F32 ? 4 : 2, WB = E * EB < 16 ? E * EB : 16;
+    constexpr int WORDS = E * EB / 4;
+    static_assert(WB == 8 || WB == 16, "");
     const char* a = reinterpret_cast<const char*>(p) + i * EB;
-    if ((reinterpret_cast<uintptr_t>(a) & 15) == 0) {
+    if ((reinterpret_cast<uintptr_t>(a) & (WB - 1)) == 0) {
+        uint32_t u[WORDS];
 #pragma unroll
-        for (int k = 0; k < E / PER; ++k) {
-            const uint4 w = __ldg(reinterpret_cast<const uint4*>(a) + k);
-            const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-            if constexpr (TYPE == SSQ_T_F32) {
-                v[2 * k] = make_float2(__uint_as_float(u[0]), __uint_as_float(u[1]));
-                v[2 * k + 1] = make_float2(__uint_as_float(u[2]), __uint_as_float(u[3]));
+        for (int k = 0; k < WORDS; k += WB / 4) {
+            if constexpr (WB == 16) {
+                const uint4 w = __ldg(reinterpret_cast<const uint4*>(a + k * 4));
+                u[k] = w.x; u[k + 1] = w.y; u[k + 2] = w.z; u[k + 3] = w.w;
             } else {
-#pragma unroll
-                for (int m = 0; m < 4; ++m) {
-                    if constexpr (TYPE == SSQ_T_BF16)
-                        v[4 * k + m] = make_float2(__uint_as_float(u[m] << 16),
-                                                   __uint_as_float(u[m] & 0xffff0000u));
-                    else
-                        v[4 * k + m] = __half22float2(*reinterpret_cast<const __half2*>(&u[m]));
-                }
+                const uint2 w = __ldg(reinterpret_cast<const uint2*>(a + k * 4));
+                u[k] = w.x; u[k + 1] = w.y;
             }
+        }
+#pragma unroll
+        for (int k = 0; k < E / 2; ++k) {
+            if constexpr (TYPE == SSQ_T_F32)
+                v[k] = make_float2(__uint_as_float(u[2 * k]), __uint_as_float(u[2 * k + 1]));
+            else if constexpr (TYPE == SSQ_T_BF16)
+                v[k] = make_float2(__uint_as_float(u[k] << 16),
+                                   __uint_as_float(u[k] & 0xffff0000u));
+            else
+                v[k] = __half22float2(*reinterpret_cast<const __half2*>(&u[k]));
         }
     } else {
 #pragma unroll
@@ -101,8 +106,8 @@ __device__ __forceinline__ void single_unit(const PoolView& pv, const RaggedCall
     const long long xat = t * rc.xs + (long long)h * pv.P;
     float xn = p < pv.P ? load_act<TYPE>(rc.x, xat + p) : 0.0f;
     const float dt = __ldg(rc.dt + t * rc.dts + h);
-    const long long Bat = t * rc.Bs + (long long)g * N + j * E;
-    const long long Cat = t * rc.Cs + (long long)g * N + j * E;
+    constexpr int PE = kPiece<RF, N> < 16 ? kPiece<RF, N> : 16;
+    const long long Bat = t * rc.Bs + (long long)g * N, Cat = t * rc.Cs + (long long)g * N;
     const float lam = decay(dt, __ldg(rc.A + h)), D = __ldg(rc.D + h);
     const float2 l2 = make_float2(lam, lam);
     for (int k = 0; k < steps; ++k) {
@@ -118,12 +123,12 @@ __device__ __forceinline__ void single_unit(const PoolView& pv, const RaggedCall
         const float2 x2 = make_float2(dtx, dtx);
         float2 acc = make_float2(0.0f, 0.0f);
 #pragma unroll
-        for (int q = 0; q < E; q += 16) {            // B and C again from L1
-            float2 Bv[8], Cv[8];
-            load_acts<TYPE, 16>(rc.B, Bat + q, Bv);
-            load_acts<TYPE, 16>(rc.C, Cat + q, Cv);
+        for (int q = 0; q < E; q += PE) {            // B and C again from L1
+            float2 Bv[PE / 2], Cv[PE / 2];
+            load_acts<TYPE, PE>(rc.B, Bat + row_entry<RF, N>(q, j), Bv);
+            load_acts<TYPE, PE>(rc.C, Cat + row_entry<RF, N>(q, j), Cv);
 #pragma unroll
-            for (int n = 0; n < 16; n += 2) {
+            for (int n = 0; n < PE; n += 2) {
                 const float2 v = fma2(l2, make_float2(s[q + n], s[q + n + 1]), mul2(x2, Bv[n / 2]));
                 s[q + n] = v.x;
                 s[q + n + 1] = v.y;
@@ -133,7 +138,7 @@ __device__ __forceinline__ void single_unit(const PoolView& pv, const RaggedCall
         const float y = grp_sum<LPR>(__fadd_rn(acc.x, acc.y));
         if (p < pv.P && j == 0)
             store_act<TYPE>(rc.y, t * rc.ys + (long long)h * pv.P + p, __fmaf_rn(D, x, y));
-        row_store<RF, N, true>(place, p, j, p < pv.P, s, reinterpret_cast<uint32_t*>(pv.pool));
+        raw_store<RF, N>(place, p, j, p < pv.P, s, reinterpret_cast<uint32_t*>(pv.pool));
         p = pn;
     }
 }
@@ -202,43 +207,34 @@ __device__ __forceinline__ void write_plan(const PoolView& pv, const RaggedCall&
     }
 }
 
-template <int FMT, int N, int TYPE>
-__global__ void __launch_bounds__(kThreads, 2)
-tokens_kernel(const __grid_constant__ PoolView pv, const __grid_constant__ RaggedCall rc,
-              int steps, int single_blocks)
+// Where entry n of B or C is staged: lane by lane, in the order in which a
+// lane holds the entries of its row.
+template <int RF, int N>
+__device__ __forceinline__ int staged_row(int n)
 {
-    if ((int)blockIdx.x < single_blocks) {
-        single_tokens<FMT, N, TYPE>(pv, rc, steps, single_blocks);
-        return;
-    }
-    int block = (int)blockIdx.x - single_blocks;
-    if (rc.plan && --block < 0) {
-        write_plan(pv, rc);
-        return;
-    }
+    constexpr int E = Shape<N>::E, LPR = Shape<N>::LPR, PE = kPiece<RF, N>;
+    const int piece = n / PE;
+    return (piece % LPR) * (E + 4) + piece / LPR * PE + n % PE;
+}
+template <int FMT, int N>
+__device__ __forceinline__ int staged_at(bool quant, int n)
+{
+    return !Fmt<FMT>::quant || quant ? staged_row<FMT, N>(n) : staged_row<SSQ_F32, N>(n);
+}
+
+// A run of several tokens on `rows` rows of one head; the whole block.
+template <int FMT, int N, int TYPE>
+__device__ __forceinline__ void run_unit(const PoolView& pv, const RaggedCall& rc, const Run& run,
+                                         int pos, int p, float (&sB)[kTok][kRowF<N>],
+                                         float (&sC)[kTok][kRowF<N>], float* sLam, float* sDt)
+{
     constexpr int E = Shape<N>::E, LPR = Shape<N>::LPR;
-    __shared__ __align__(16) float sB[kTok][kRowF<N>], sC[kTok][kRowF<N>];
-    __shared__ float sLam[kTok], sDt[kTok];
-
-    const int rows = blockDim.x / LPR;
-    const int tiles = (pv.P + rows - 1) / rows;
-    const int per = tiles * pv.H;
-    const int b = block / per;
-    const int unit = block - b * per;
-    const int tile = unit % tiles;
-    const int pos = unit / tiles;                  // region position of the head
-    const int h = pv.perm[pos];
-    const int tid = threadIdx.x;
-    const Run run = ragged_run(pv, rc, b, false);
-    if (!run.ok || run.len >= rc.chunk_min || run.len == 1) return;
-    if (run.len == 0 && !run.fresh) return;
-
-    const int j = tid % LPR;
-    const int p = tile * rows + tid / LPR;
+    const int tid = threadIdx.x, j = tid % LPR;
     const bool active = p < pv.P;
-    const int g = h / pv.hpg;
+    const int h = pv.perm[pos], g = h / pv.hpg;
     const float A = __ldg(rc.A + h), D = __ldg(rc.D + h);
     const RowPlace place = place_head<FMT>(pv, run.slot, rc.layer, pos);
+    const long long at = (long long)h * pv.P + p;
 
     float s[E];
     if (run.fresh) {
@@ -247,26 +243,30 @@ tokens_kernel(const __grid_constant__ PoolView pv, const __grid_constant__ Ragge
     } else {
         row_load<FMT, N>(place, p, j, active, s);
     }
-
     for (int c0 = 0; c0 < run.len; c0 += kTok) {
         const int nt = min(kTok, run.len - c0);
         const long long t0 = (long long)run.t0 + c0;
-        if (c0) __syncthreads();
+        __syncthreads();
         for (int i = tid; i < nt * N; i += blockDim.x) {
             const int t = i / N, n = i % N;
-            const int at = (n / E) * (E + 4) + n % E;
-            sB[t][at] = load_act<TYPE>(rc.B, (t0 + t) * rc.Bs + (long long)g * N + n);
-            sC[t][at] = load_act<TYPE>(rc.C, (t0 + t) * rc.Cs + (long long)g * N + n);
+            const int to = staged_at<FMT, N>(place.quant, n);
+            sB[t][to] = load_act<TYPE>(rc.B, (t0 + t) * rc.Bs + (long long)g * N + n);
+            sC[t][to] = load_act<TYPE>(rc.C, (t0 + t) * rc.Cs + (long long)g * N + n);
         }
         if (tid < nt) {
             const float dt = __ldg(rc.dt + (t0 + tid) * rc.dts + h);
             sDt[tid] = dt;
             sLam[tid] = decay(dt, A);
         }
+        float xs[kTok];
+#pragma unroll
+        for (int t = 0; t < kTok; ++t)
+            xs[t] = active && t < nt ? load_act<TYPE>(rc.x, (t0 + t) * rc.xs + at) : 0.0f;
         __syncthreads();
-        for (int t = 0; t < nt; ++t) {
-            const long long at = (long long)h * pv.P + p;
-            const float x = active ? load_act<TYPE>(rc.x, (t0 + t) * rc.xs + at) : 0.0f;
+#pragma unroll
+        for (int t = 0; t < kTok; ++t) {
+            if (t >= nt) break;
+            const float x = xs[t];
             const float dtx = __fmul_rn(sDt[t], x);
             const float lam = sLam[t];
             const float4* Bp = reinterpret_cast<const float4*>(&sB[t][j * (E + 4)]);
@@ -291,38 +291,83 @@ tokens_kernel(const __grid_constant__ PoolView pv, const __grid_constant__ Ragge
     row_store<FMT, N>(place, p, j, active, s, reinterpret_cast<uint32_t*>(pv.pool));
 }
 
+// Every block takes its share of the single tokens, then of the other runs
+// that do not go through chunks; block 0 first writes the chunk kernel's list.
+template <int FMT, int N, int TYPE>
+__global__ void __launch_bounds__(kThreads, 2)
+tokens_kernel(const __grid_constant__ PoolView pv, const __grid_constant__ RaggedCall rc,
+              int steps)
+{
+    constexpr int LPR = Shape<N>::LPR;
+    __shared__ __align__(16) float sB[kTok][kRowF<N>], sC[kTok][kRowF<N>];
+    __shared__ float sLam[kTok], sDt[kTok];
+    __shared__ int list[kThreads], count[kThreads / 32];
+
+    if (rc.plan && blockIdx.x == 0) write_plan(pv, rc);
+    single_tokens<FMT, N, TYPE>(pv, rc, steps, gridDim.x);
+
+    const int tid = threadIdx.x;
+    const int rows = blockDim.x / LPR;
+    const int tiles = (pv.P + rows - 1) / rows, per = tiles * pv.H;
+    int skip = blockIdx.x;                           // units until this block's next one
+    for (int b0 = 0; b0 < rc.batch; b0 += blockDim.x) {
+        // the runs among the next blockDim.x requests
+        __syncthreads();
+        bool take = false;
+        if (b0 + tid < rc.batch) {
+            const Run run = ragged_run(pv, rc, b0 + tid, false);
+            take = run.ok && run.len < rc.chunk_min && run.len != 1 && (run.len > 0 || run.fresh);
+        }
+        const unsigned mine = __ballot_sync(0xffffffffu, take);
+        if (tid % 32 == 0) count[tid / 32] = __popc(mine);
+        if (!__syncthreads_or(take)) continue;
+        int found = 0, before = 0;
+        for (int w = 0; w < (int)blockDim.x / 32; ++w) {
+            if (w < tid / 32) before += count[w];
+            found += count[w];
+        }
+        if (take) list[before + __popc(mine & ((1u << tid % 32) - 1))] = b0 + tid;
+        __syncthreads();
+        const int units = found * per;
+        for (; skip < units; skip += gridDim.x) {
+            const int b = list[skip / per], unit = skip % per;
+            const Run run = ragged_run(pv, rc, b, false);
+            run_unit<FMT, N, TYPE>(pv, rc, run, unit / tiles, unit % tiles * rows + tid / LPR, sB,
+                                   sC, sLam, sDt);
+        }
+        skip -= units;
+    }
+}
+
 template <int FMT, int N>
 cudaError_t launch_n(const PoolView& pv, const RaggedCall& rc, cudaStream_t st)
 {
     constexpr int LPR = Shape<N>::LPR;
-    // Single tokens: warps of up to 8 groups of rows each, on a grid that is
-    // resident at once (two blocks per SM).
-    constexpr int kWarps = kThreads / 32;
+    // Blocks of whole warps over a head's rows, on a grid that is resident at
+    // once (two blocks per SM).
+    int threads = (pv.P * LPR + 31) / 32 * 32;
+    if (threads > kThreads) threads = kThreads;
+    const int rows = threads / LPR, warps = threads / 32;
     const long long resident = 2LL * kSMs;
+    // Single tokens: a warp takes up to 8 groups of rows of a head, fewer where
+    // that would leave warps without work.
     const long long groups = (long long)((pv.P + Shape<N>::RPW - 1) / Shape<N>::RPW) * pv.H
                              * rc.batch;
     int steps = 8;
-    while (steps > 1 && groups < resident * kWarps * steps) steps /= 2;
+    while (steps > 1 && groups < resident * warps * steps) steps /= 2;
     const int rows1 = steps * Shape<N>::RPW;
     const long long units = (long long)((pv.P + rows1 - 1) / rows1) * pv.H * rc.batch;
-    long long single = (units + kWarps - 1) / kWarps;
-    if (single > resident) single = resident;
-    // Runs of several tokens: blocks of whole warps over a head's rows.  Runs
-    // of no token (a fresh slot is zeroed) go with them.
-    int threads = (pv.P * LPR + 31) / 32 * 32;
-    if (threads > kThreads) threads = kThreads;
-    const int rows = threads / LPR;
-    const long long blocks = (long long)((pv.P + rows - 1) / rows) * pv.H * rc.batch;
-    if (blocks + single > 0x7ffffff0LL) return cudaErrorInvalidConfiguration;
-    const unsigned grid = (unsigned)(single + (rc.plan ? 1 : 0) + blocks);
-    const int sb = (int)single;
+    long long blocks = (units + warps - 1) / warps;
+    if (rc.max_len != 1) {
+        const long long runs = (long long)((pv.P + rows - 1) / rows) * pv.H * rc.batch;
+        if (runs > 0x3fffffffLL) return cudaErrorInvalidConfiguration;
+        if (blocks < runs) blocks = runs;
+    }
+    const unsigned grid = (unsigned)(blocks < resident ? blocks : resident);
     switch (rc.type) {
-    case SSQ_T_BF16:
-        tokens_kernel<FMT, N, SSQ_T_BF16><<<grid, threads, 0, st>>>(pv, rc, steps, sb); break;
-    case SSQ_T_F16:
-        tokens_kernel<FMT, N, SSQ_T_F16><<<grid, threads, 0, st>>>(pv, rc, steps, sb); break;
-    default:
-        tokens_kernel<FMT, N, SSQ_T_F32><<<grid, threads, 0, st>>>(pv, rc, steps, sb); break;
+    case SSQ_T_BF16: tokens_kernel<FMT, N, SSQ_T_BF16><<<grid, threads, 0, st>>>(pv, rc, steps); break;
+    case SSQ_T_F16: tokens_kernel<FMT, N, SSQ_T_F16><<<grid, threads, 0, st>>>(pv, rc, steps); break;
+    default: tokens_kernel<FMT, N, SSQ_T_F32><<<grid, threads, 0, st>>>(pv, rc, steps); break;
     }
     return cudaGetLastError();
 }

@@ -1,6 +1,11 @@
 // ssq_rowio.cuh -- a state row between the pool and registers: E = min(32, N)
-// consecutive entries per lane, LPR = N/E lanes per row, in the six storage
-// formats, with the refit and rounding of ssq_common.cuh.
+// entries per lane, LPR = N/E lanes per row, in the six storage formats, with
+// the refit and rounding of ssq_common.cuh.
+//
+// The lanes of a row take its 16-byte pieces in turn, so that a load or store
+// instruction of a warp covers whole lines (with E consecutive entries per
+// lane an fp32 row's pieces lay 128 bytes apart, and 256 single tokens of 24
+// fp32 heads took 139 us).
 #pragma once
 
 #include "ssq_common.cuh"
@@ -32,6 +37,17 @@ __device__ __forceinline__ RowPlace place_head(const PoolView& pv, int slot, int
     return rp;
 }
 
+// Entries of a 16-byte piece in row format RF, and the row's entry that lane j
+// holds at local index n.
+template <int RF, int N>
+constexpr int kPiece = 128 / Fmt<RF>::bits < Shape<N>::E ? 128 / Fmt<RF>::bits : Shape<N>::E;
+template <int RF, int N>
+__device__ __forceinline__ constexpr int row_entry(int n, int j)
+{
+    constexpr int PE = kPiece<RF, N>;
+    return (n / PE * Shape<N>::LPR + j) * PE + n % PE;
+}
+
 // A lane's part of a row as it is stored, RF the format of the row (fp rows of
 // the integer formats are SSQ_F32): loaded at one point, decoded at another.
 template <int RF, int N>
@@ -51,7 +67,7 @@ struct RawRow {
         z = 0.0f;
         if (!active) return;
         const uint8_t* rows = F::quant ? rp.codes : rp.fp;
-        load_chunk<CB>(c, rows + (long long)p * (N * F::bits / 8) + j * CB);
+        piece_io<true>(const_cast<uint8_t*>(rows) + (long long)p * (N * F::bits / 8), j);
         if constexpr (F::quant) {
             if constexpr (F::sym) {
                 delta = __ldcs(reinterpret_cast<const float*>(rp.meta) + p);
@@ -59,6 +75,26 @@ struct RawRow {
                 const float2 m = __ldcs(reinterpret_cast<const float2*>(rp.meta) + p);
                 delta = m.x;
                 z = m.y;
+            }
+        }
+    }
+    // The lane's pieces of the row that starts at `row`.
+    template <bool LOAD>
+    __device__ __forceinline__ void piece_io(uint8_t* row, int j)
+    {
+        constexpr int PB = kPiece<RF, N> * F::bits / 8;      // 16, or a whole part below that
+#pragma unroll
+        for (int i = 0; i < CB / PB; ++i) {
+            Chunk<PB> q;
+            uint8_t* at = row + (i * Shape<N>::LPR + j) * PB;
+            if constexpr (LOAD) {
+                load_chunk<PB>(q, at);
+#pragma unroll
+                for (int k = 0; k < PB / 4; ++k) c.w[i * (PB / 4) + k] = q.w[k];
+            } else {
+#pragma unroll
+                for (int k = 0; k < PB / 4; ++k) q.w[k] = c.w[i * (PB / 4) + k];
+                store_chunk<PB>(at, q);
             }
         }
     }
@@ -78,8 +114,8 @@ struct RawRow {
     }
 };
 
-// Entries [j*E, j*E+E) of row p as fp32.  Every lane of the warp calls this
-// with the same head.
+// The lane's entries of row p as fp32.  Every lane of the warp calls this with
+// the same head.
 template <int FMT, int N>
 __device__ __forceinline__ void row_load(const RowPlace& rp, int p, int j, bool active,
                                          float (&s)[Shape<N>::E])
@@ -97,60 +133,106 @@ __device__ __forceinline__ void row_load(const RowPlace& rp, int p, int j, bool 
     r.decode(s);
 }
 
-// Refit, round and store row p (fp rows: convert and store).  Every lane of
-// the warp calls this; lanes that are not `active` store nothing.
-template <int FMT, int N, bool ALL_QUANT = false>
+// Refit, round and store row p of format RF.  Every lane of the warp calls
+// this; lanes that are not `active` store nothing.
+template <int RF, int N>
+__device__ __forceinline__ void raw_store(const RowPlace& rp, int p, int j, bool active,
+                                          const float (&s)[Shape<N>::E], uint32_t* err)
+{
+    using F = Fmt<RF>;
+    constexpr int E = Shape<N>::E, LPR = Shape<N>::LPR;
+    RawRow<RF, N> raw;
+    if constexpr (F::quant) {
+        RowParams q = refit_row<RF, E, LPR>(s);
+        // min and max pass over NaN entries; a sum of zeros does not
+        float2 bad = make_float2(0.0f, 0.0f);
+#pragma unroll
+        for (int n = 0; n < E; n += 2)
+            bad = fma2(make_float2(s[n], s[n + 1]), make_float2(0.0f, 0.0f), bad);
+        if (!(grp_sum<LPR>(__fadd_rn(bad.x, bad.y)) == 0.0f)) {
+            // the row then decodes to NaN
+            q.finite = false;
+            q.delta = __int_as_float(0x7fffffff);
+        }
+        float r[E];
+        uint32_t k[E];
+        round_row<RF, E>(q, s, r, k);
+        pack_codes<RF, E>(k, raw.c);
+        if (!active) return;
+        raw.template piece_io<false>(rp.codes + (long long)p * (N * F::bits / 8), j);
+        if (j == 0) {
+            if constexpr (F::sym)
+                reinterpret_cast<float*>(rp.meta)[p] = q.delta;
+            else
+                reinterpret_cast<float2*>(rp.meta)[p] = make_float2(q.delta, q.z);
+            if (!q.finite) atomicOr(err, SSQ_DEVERR_NONFINITE);
+        }
+    } else {
+        if (!active) return;
+#pragma unroll
+        for (int i = 0; i < raw.CB / 4; ++i) {
+            if constexpr (RF == SSQ_BF16)
+                raw.c.w[i] = (uint32_t)__bfloat16_as_ushort(__float2bfloat16_rn(s[2 * i]))
+                             | ((uint32_t)__bfloat16_as_ushort(__float2bfloat16_rn(s[2 * i + 1])) << 16);
+            else
+                raw.c.w[i] = __float_as_uint(s[i]);
+        }
+        raw.template piece_io<false>(rp.fp + (long long)p * (N * F::bits / 8), j);
+    }
+}
+
+// The same for a head of a pool of format FMT.
+template <int FMT, int N>
 __device__ __forceinline__ void row_store(const RowPlace& rp, int p, int j, bool active,
                                           const float (&s)[Shape<N>::E], uint32_t* err)
 {
-    using F = Fmt<FMT>;
-    constexpr int E = Shape<N>::E, LPR = Shape<N>::LPR;
-    if constexpr (F::quant) {
-        if (ALL_QUANT || rp.quant) {
-            constexpr int CB = E * F::bits / 8;
-            RowParams q = refit_row<FMT, E, LPR>(s);
-            // min and max pass over NaN entries; a sum of zeros does not
-            float2 bad = make_float2(0.0f, 0.0f);
-#pragma unroll
-            for (int n = 0; n < E; n += 2)
-                bad = fma2(make_float2(s[n], s[n + 1]), make_float2(0.0f, 0.0f), bad);
-            if (!(grp_sum<LPR>(__fadd_rn(bad.x, bad.y)) == 0.0f)) {
-                // the row then decodes to NaN
-                q.finite = false;
-                q.delta = __int_as_float(0x7fffffff);
-            }
-            float r[E];
-            uint32_t k[E];
-            Chunk<CB> c;
-            round_row<FMT, E>(q, s, r, k);
-            pack_codes<FMT, E>(k, c);
-            if (active) {
-                store_chunk<CB>(rp.codes + (long long)p * (N * F::bits / 8) + j * CB, c);
-                if (j == 0) {
-                    if constexpr (F::sym)
-                        reinterpret_cast<float*>(rp.meta)[p] = q.delta;
-                    else
-                        reinterpret_cast<float2*>(rp.meta)[p] = make_float2(q.delta, q.z);
-                    if (!q.finite) atomicOr(err, SSQ_DEVERR_NONFINITE);
-                }
-            }
+    if constexpr (Fmt<FMT>::quant) {
+        if (!rp.quant) {
+            raw_store<SSQ_F32, N>(rp, p, j, active, s, err);
             return;
         }
     }
-    if (!active) return;
-    if constexpr (FMT == SSQ_BF16) {
-        Chunk<E * 2> c;
+    raw_store<FMT, N>(rp, p, j, active, s, err);
+}
+
+// The lane's entries to and from a row of fp32 in entry order.
+template <int RF, int N, bool TO>
+__device__ __forceinline__ void stage_io(float (&s)[Shape<N>::E], int j, float* row)
+{
 #pragma unroll
-        for (int n = 0; n < E; n += 2)
-            c.w[n / 2] = (uint32_t)__bfloat16_as_ushort(__float2bfloat16_rn(s[n]))
-                         | ((uint32_t)__bfloat16_as_ushort(__float2bfloat16_rn(s[n + 1])) << 16);
-        store_chunk<E * 2>(rp.fp + ((long long)p * N + j * E) * 2, c);
-    } else {
-        Chunk<E * 4> c;
-#pragma unroll
-        for (int n = 0; n < E; ++n) c.w[n] = __float_as_uint(s[n]);
-        store_chunk<E * 4>(rp.fp + ((long long)p * N + j * E) * 4, c);
+    for (int n = 0; n < Shape<N>::E; n += 4) {
+        float4* at = reinterpret_cast<float4*>(row + row_entry<RF, N>(n, j));
+        if constexpr (TO) {
+            *at = make_float4(s[n], s[n + 1], s[n + 2], s[n + 3]);
+        } else {
+            const float4 v = *at;
+            s[n] = v.x; s[n + 1] = v.y; s[n + 2] = v.z; s[n + 3] = v.w;
+        }
     }
+}
+template <int FMT, int N>
+__device__ __forceinline__ void row_to_stage(const RowPlace& rp, float (&s)[Shape<N>::E], int j,
+                                             float* row)
+{
+    if constexpr (Fmt<FMT>::quant) {
+        if (!rp.quant) {
+            stage_io<SSQ_F32, N, true>(s, j, row);
+            return;
+        }
+    }
+    stage_io<FMT, N, true>(s, j, row);
+}
+template <int FMT, int N>
+__device__ __forceinline__ void row_from_stage(const RowPlace& rp, float (&s)[Shape<N>::E], int j,
+                                               const float* row)
+{
+    if constexpr (Fmt<FMT>::quant) {
+        if (!rp.quant) {
+            stage_io<SSQ_F32, N, false>(s, j, const_cast<float*>(row));
+            return;
+        }
+    }
+    stage_io<FMT, N, false>(s, j, const_cast<float*>(row));
 }
 
 }  // namespace ssq

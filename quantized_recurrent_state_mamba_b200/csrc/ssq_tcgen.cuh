@@ -71,6 +71,21 @@ __device__ __forceinline__ void wait_ld(float (&v)[16])
                    "+f"(v[6]), "+f"(v[7]), "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]),
                    "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15]));
 }
+// 8 columns; two such arrays are valid after wait_ld8 on both.
+__device__ __forceinline__ void ld8(uint32_t taddr, float (&v)[8])
+{
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]),
+                   "=f"(v[6]), "=f"(v[7])
+                 : "r"(taddr));
+}
+__device__ __forceinline__ void wait_ld8(float (&v)[8], float (&u)[8])
+{
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]),
+                   "+f"(v[6]), "+f"(v[7]), "+f"(u[0]), "+f"(u[1]), "+f"(u[2]), "+f"(u[3]),
+                   "+f"(u[4]), "+f"(u[5]), "+f"(u[6]), "+f"(u[7]));
+}
 // v was loaded before a wait_ld of another array: its uses stay behind it.
 __device__ __forceinline__ void after_wait(float (&v)[16])
 {
