@@ -27,6 +27,7 @@
 #include <cuda_fp16.h>
 
 #include "ssq_common.cuh"
+#include "ssq_pipe.cuh"
 #include "ssq_serve_params.h"
 
 namespace ssq {
@@ -39,6 +40,17 @@ constexpr int kBThreads = 512;
 constexpr int kBWarps = kBThreads / 32;
 constexpr int kMaxTasks = SSQ_MAX_BEAMS;         // lists of a block
 constexpr float kLog2e = 1.4426950408889634f;
+
+__device__ __forceinline__ void cpa_commit()
+{
+    asm volatile("cp.async.commit_group;" ::: "memory");
+}
+// All but this thread's newest N groups have landed.
+template <int N>
+__device__ __forceinline__ void cpa_wait()
+{
+    asm volatile("cp.async.wait_group %0;" :: "n"(N) : "memory");
+}
 
 // The list's order: larger value first, then lower index.
 template <typename V>
@@ -137,7 +149,10 @@ struct TopList {
 // appended before any of them is merged, so that what equals the list's last
 // entry and comes later in the row is never let in.
 constexpr int kBuf = 32 + 256;
+// Vectors of a warp (32 x 16 bytes) on their way from global memory.
+constexpr int kAhead = 8;
 struct Buffer {
+    uint4 ring[kAhead * 32];
     float v[kBuf];
     int i[kBuf];
 };
@@ -230,12 +245,12 @@ struct Sum {
     }
 };
 
+// A block's results per task (a warp's part of a row); the lists of logits,
+// nsel apart, follow behind WarpShared: float [tasks][nsel], int [tasks][nsel].
 struct BeamShared {
-    float v[kMaxTasks * SSQ_MAX_BEAMS];   // lists of logits, nsel apart
-    int i[kMaxTasks * SSQ_MAX_BEAMS];
     double sum[kMaxTasks];                // sum of exponentials relative to max
-    float max[kMaxTasks];
     double lse[SSQ_MAX_BEAMS];
+    float max[kMaxTasks];
 };
 // The buffers of the scan, later the lists of the last merge.
 union WarpShared {
@@ -251,10 +266,13 @@ __global__ void __launch_bounds__(kBThreads, 2)
 beam_kernel(const __grid_constant__ BeamCall bc)
 {
     using T = Act<TYPE>;
-    constexpr int VEC = T::VEC, U = 4;
+    constexpr int VEC = T::VEC;
     extern __shared__ __align__(16) unsigned char smem_raw[];
     BeamShared& sh = *reinterpret_cast<BeamShared*>(smem_raw);
     WarpShared& ws = *reinterpret_cast<WarpShared*>(smem_raw + sizeof(BeamShared));
+    const int tasks = bc.beams <= kBWarps ? kBWarps / bc.beams * bc.beams : bc.beams;
+    float* list_v = reinterpret_cast<float*>(smem_raw + sizeof(BeamShared) + sizeof(WarpShared));
+    int* list_i = reinterpret_cast<int*>(list_v + tasks * bc.nsel);
 
     cg::cluster_group cluster = cg::this_cluster();
     const int CS = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
@@ -286,75 +304,82 @@ beam_kernel(const __grid_constant__ BeamCall bc)
             const int nvec = (n - head) / VEC;
             const int tail0 = head + nvec * VEC;
             const int first = (int)lo;
-            auto edge = [&](int from, int to) {   // at most VEC - 1 logits
-                float f[1] = {-INFINITY};
-                if (from + lane < to) f[0] = fmaxf(T::one(base, from + lane), -INFINITY);
-                sum.add(f, f[0]);
-                top.merge_any(f[0], f[0] == -INFINITY ? 0x7fffffff : first + from + lane);
-            };
-            if (head > 0) edge(0, head);
             const uint4* vp = reinterpret_cast<const uint4*>(base + (long long)head * T::BYTES);
             Buffer& buf = ws.buf[warp];
+            const int blocks = (nvec + 31) / 32;     // vectors of the whole warp
+            auto fetch = [&](int v) {                // one group per call, empty past the end
+                const int at = v * 32 + lane;
+                if (at < nvec) cpa16(&buf.ring[v % kAhead * 32 + lane], vp + at);
+                cpa_commit();
+            };
+#pragma unroll
+            for (int v = 0; v < kAhead; ++v) fetch(v);
             int held = 0;
-            auto flush = [&](int least) {         // merge while `least` entries are held
+            auto append = [&](bool in, float f, int i) {
+                const unsigned m = __ballot_sync(0xffffffffu, in);
+                if (in) {
+                    const int to = held + __popc(m & ((1u << lane) - 1));
+                    buf.v[to] = f;
+                    buf.i[to] = i;
+                }
+                held += __popc(m);
+            };
+            auto flush = [&](int least) {            // merge while `least` entries are held
+                __syncwarp();
                 while (held >= least) {
-                    const int e = held - 32 + lane;      // the last 32 (or fewer)
+                    const int e = held - 32 + lane;  // the last 32 (or fewer)
                     top.merge_any(e >= 0 ? buf.v[e] : -INFINITY,
                                   e >= 0 ? buf.i[e] : 0x7fffffff);
                     held = max(0, held - 32);
                 }
                 __syncwarp();
             };
-            // NaN counts as -inf
-            auto take = [&](uint4 w, int at, bool inside) {
+            auto edge = [&](int from, int to) {      // at most VEC - 1 logits; NaN is -inf
+                float f[1] = {-INFINITY};
+                if (from + lane < to) f[0] = fmaxf(T::one(base, from + lane), -INFINITY);
+                sum.add(f, f[0]);
+                append(f[0] > top.tv, f[0], first + from + lane);
+            };
+            if (head > 0) edge(0, head);
+            for (int v = 0; v < blocks; ++v) {
+                cpa_wait<kAhead - 1>();
                 float f[VEC];
-                T::unpack(w, f);
+                T::unpack(buf.ring[v % kAhead * 32 + lane], f);
+                fetch(v + kAhead);                   // (this lane's own place)
+                const int at = v * 32 + lane;
+                if (v == blocks - 1 && at >= nvec) {
+#pragma unroll
+                    for (int k = 0; k < VEC; ++k) f[k] = -INFINITY;
+                }
                 float mx = -INFINITY;
 #pragma unroll
                 for (int k = 0; k < VEC; ++k) {
-                    f[k] = inside ? fmaxf(f[k], -INFINITY) : -INFINITY;
+                    f[k] = fmaxf(f[k], -INFINITY);   // NaN: -inf
                     mx = fmaxf(mx, f[k]);
                 }
                 sum.add(f, mx);
-                if (__any_sync(0xffffffffu, mx > top.tv)) {
-                    const int i0 = first + head + at * VEC;
+                const int i0 = first + head + at * VEC;
+                if (v == 0) {
+                    // At least nsel logits are as large as the nsel-th largest
+                    // of the lanes' maxima: the list starts from those.
+                    float least = mx;
+                    int who = lane;
+                    sort32(least, who);
+                    least = nsel <= 32 ? __shfl_sync(0xffffffffu, least, (nsel - 1) & 31)
+                                       : -INFINITY;
 #pragma unroll
-                    for (int k = 0; k < VEC; ++k) {
-                        const bool in = f[k] > top.tv;
-                        const unsigned m = __ballot_sync(0xffffffffu, in);
-                        if (in) {
-                            const int to = held + __popc(m & ((1u << lane) - 1));
-                            buf.v[to] = f[k];
-                            buf.i[to] = i0 + k;
-                        }
-                        held += __popc(m);
-                    }
-                    __syncwarp();
+                    for (int k = 0; k < VEC; ++k)
+                        append(f[k] >= least && f[k] > -INFINITY, f[k], i0 + k);
+                    flush(1);
+                } else if (__any_sync(0xffffffffu, mx > top.tv)) {
+#pragma unroll
+                    for (int k = 0; k < VEC; ++k) append(f[k] > top.tv, f[k], i0 + k);
                     flush(32);
                 }
-            };
-            int v0 = 0;
-            for (; v0 + 32 * U <= nvec; v0 += 32 * U) {
-                uint4 w[U];
-#pragma unroll
-                for (int u = 0; u < U; ++u) w[u] = __ldcs(vp + v0 + u * 32 + lane);
-#pragma unroll
-                for (int u = 0; u < U; ++u) take(w[u], v0 + u * 32 + lane, true);
             }
-            if (v0 < nvec) {
-                uint4 w[U];
-#pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    const int at = v0 + u * 32 + lane;
-                    w[u] = make_uint4(0, 0, 0, 0);
-                    if (at < nvec) w[u] = __ldcs(vp + at);
-                }
-#pragma unroll
-                for (int u = 0; u < U; ++u)
-                    if (v0 + u * 32 < nvec) take(w[u], v0 + u * 32 + lane, v0 + u * 32 + lane < nvec);
-            }
-            flush(1);
             if (tail0 < n) edge(tail0, n);
+            flush(1);
+            cpa_wait<0>();
         }
         // the warp's maximum and sum
         float m = sum.m;
@@ -370,8 +395,8 @@ beam_kernel(const __grid_constant__ BeamCall bc)
 #pragma unroll
         for (int k = 0; k < KP; ++k)
             if (lane + 32 * k < nsel) {
-                sh.v[task * nsel + lane + 32 * k] = top.v[k];
-                sh.i[task * nsel + lane + 32 * k] = top.i[k];
+                list_v[task * nsel + lane + 32 * k] = top.v[k];
+                list_i[task * nsel + lane + 32 * k] = top.i[k];
             }
     }
     __syncthreads();
@@ -389,8 +414,8 @@ beam_kernel(const __grid_constant__ BeamCall bc)
                 const int e = lane + 32 * k;
                 if (32 * k >= nsel) break;
                 const bool has = e < nsel;
-                top.merge(has ? sh.v[t * nsel + e] : -INFINITY,
-                          has ? sh.i[t * nsel + e] : 0x7fffffff);
+                top.merge(has ? list_v[t * nsel + e] : -INFINITY,
+                          has ? list_i[t * nsel + e] : 0x7fffffff);
             }
         }
         double s = 0.0;
@@ -406,35 +431,34 @@ beam_kernel(const __grid_constant__ BeamCall bc)
 #pragma unroll
         for (int k = 0; k < KP; ++k)
             if (lane + 32 * k < nsel) {
-                sh.v[t0 * nsel + lane + 32 * k] = top.v[k];
-                sh.i[t0 * nsel + lane + 32 * k] = top.i[k];
+                list_v[t0 * nsel + lane + 32 * k] = top.v[k];
+                list_i[t0 * nsel + lane + 32 * k] = top.i[k];
             }
     }
     cluster.sync();
 
     if (rank == 0) {
-        if (tid < K) {
-            double lse = 0.0;     // finished beams: the value is the score
-            if (!(bc.done && bc.done[(long long)req * K + tid])) {
-                float m = -INFINITY;
-                for (int q = 0; q < CS; ++q)
-                    m = fmaxf(m, cluster.map_shared_rank(&sh, q)->max[tid * wpr]);
-                double s = 0.0;
-                for (int q = 0; q < CS; ++q) {
-                    const BeamShared* o = cluster.map_shared_rank(&sh, q);
-                    const float mq = o->max[tid * wpr];
-                    if (mq != -INFINITY) s += o->sum[tid * wpr] * exp((double)mq - (double)m);
-                }
-                lse = (double)m + log(s);
-            }
-            sh.lse[tid] = lse;
+        for (int row = warp; row < K; row += kBWarps) {   // lane q: block q's part (CS <= 32)
+            const BeamShared* o = cluster.map_shared_rank(&sh, min(lane, CS - 1));
+            const float mq = lane < CS ? o->max[row * wpr] : -INFINITY;
+            const double sq = lane < CS ? o->sum[row * wpr] : 0.0;
+            float m = mq;
+#pragma unroll
+            for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+            double s = mq == -INFINITY ? 0.0 : sq * exp((double)mq - (double)m);
+#pragma unroll
+            for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
+            // finished beams: the value is the score
+            const bool done = bc.done && bc.done[(long long)req * K + row];
+            if (lane == 0) sh.lse[row] = done ? 0.0 : (double)m + log(s);
         }
         __syncthreads();
         TopList<double, KP> best;
         best.clear(nsel);
         for (int li = warp; li < K * CS; li += kBWarps) {
             const int q = li / K, row = li - q * K;
-            const BeamShared* o = cluster.map_shared_rank(&sh, q);
+            const float* ov = cluster.map_shared_rank(list_v, q);
+            const int* oi = cluster.map_shared_rank(list_i, q);
             const double sc = (double)__ldg(bc.scores + (long long)req * K + row);
             const double lse = sh.lse[row];
 #pragma unroll
@@ -442,13 +466,19 @@ beam_kernel(const __grid_constant__ BeamCall bc)
                 const int e = lane + 32 * k;
                 if (32 * k >= nsel) break;
                 const bool has = e < nsel;
-                const int i = has ? o->i[row * wpr * nsel + e] : 0x7fffffff;
+                const int i = has ? oi[row * wpr * nsel + e] : 0x7fffffff;
                 double val = i == 0x7fffffff
-                    ? -INFINITY : sc + ((double)o->v[row * wpr * nsel + e] - lse);
+                    ? -INFINITY : sc + ((double)ov[row * wpr * nsel + e] - lse);
                 // NaN: a score or a row without a finite sum
                 const bool valid = val > -INFINITY;
-                // (sorted again: logits that differ may give equal values)
-                best.merge_any(valid ? val : -INFINITY, valid ? row * V + i : 0x7fffffff);
+                if (!valid) val = -INFINITY;
+                int flat = valid ? row * V + i : 0x7fffffff;
+                // logits that differ may give equal values: then sort again
+                const double nv = __shfl_down_sync(0xffffffffu, val, 1);
+                const int ni = __shfl_down_sync(0xffffffffu, flat, 1);
+                if (__any_sync(0xffffffffu, lane < 31 && better(nv, ni, val, flat)))
+                    sort32(val, flat);
+                best.merge(val, flat);
             }
         }
         // the warps' lists two by two
@@ -494,9 +524,20 @@ template <int TYPE, int KP>
 cudaError_t launch_one(const BeamCall& bc, int cs, cudaStream_t st)
 {
     auto kern = beam_kernel<TYPE, KP>;
-    constexpr int smem = (int)(sizeof(BeamShared) + sizeof(WarpShared));
-    thread_local int done = -1;
-    cudaError_t e = allow_smem(kern, smem, &done);
+    constexpr int fixed = (int)(sizeof(BeamShared) + sizeof(WarpShared));
+    constexpr int most = fixed + kMaxTasks * SSQ_MAX_BEAMS * 8;
+    const int tasks = bc.beams <= kBWarps ? kBWarps / bc.beams * bc.beams : bc.beams;
+    const int smem = fixed + tasks * bc.nsel * 8;
+    thread_local int done = -1, done16 = -1;
+    cudaError_t e = allow_smem(kern, most, &done);
+    if (e == cudaSuccess && cs > 8) {
+        int dev = 0;
+        e = cudaGetDevice(&dev);
+        if (e == cudaSuccess && done16 != dev) {
+            e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+            if (e == cudaSuccess) done16 = dev;
+        }
+    }
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(bc.batch * cs));
@@ -517,12 +558,15 @@ cudaError_t launch_one(const BeamCall& bc, int cs, cudaStream_t st)
 
 cudaError_t launch_beam(const BeamCall& bc, cudaStream_t st)
 {
-    // Blocks per request: as many (up to the portable cluster size) as keep
-    // the batch within two blocks per SM and leave every warp a vector.
+    // Blocks per request (a cluster): as many as keep the batch within two
+    // blocks per SM and leave every warp a vector; 16, which must find 16 SMs
+    // of one GPC at once, only for batches that fill few GPCs (1 x 4 beams of
+    // 32000 logits: @@ us with 16, @@ with 8; 16 x 5 of 50001: 47 with 16, 28
+    // with 8).
     const int vec = bc.type == SSQ_T_F32 ? 4 : 8;
     const long long vectors = (long long)bc.beams * bc.vocab / vec;
     int cs = 1;
-    while (cs < 8 && (long long)bc.batch * cs * 2 <= 2 * kSMs
+    while (cs < (bc.batch <= 4 ? 16 : 8) && (long long)bc.batch * cs * 2 <= 2 * kSMs
            && vectors >= (long long)cs * 2 * kBThreads)
         cs *= 2;
     const bool two = bc.nsel > 32;
