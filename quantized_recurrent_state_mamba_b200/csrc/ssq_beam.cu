@@ -59,6 +59,24 @@ __device__ __forceinline__ bool better(V a, int ia, V b, int ib)
     return a > b || (a == b && ia < ib);
 }
 
+// Doubles as integers of the same order (the merges compare a lot, and the
+// double-precision pipe is slow at it).  NaN does not occur.
+__device__ __forceinline__ long long order_of(double v)
+{
+    const long long b = __double_as_longlong(v);
+    return b ^ ((b >> 63) & 0x7fffffffffffffffLL);
+}
+__device__ __forceinline__ double value_of(long long k)
+{
+    return __longlong_as_double(k ^ ((k >> 63) & 0x7fffffffffffffffLL));
+}
+template <typename V>
+__device__ __forceinline__ V nothing();             // -inf
+template <>
+__device__ __forceinline__ float nothing<float>() { return -INFINITY; }
+template <>
+__device__ __forceinline__ long long nothing<long long>() { return (long long)0x800fffffffffffffULL; }
+
 // The better of two entries goes to lane i, the other to lane i ^ o, in the
 // lanes where `up` holds; the other way round elsewhere.
 template <typename V>
@@ -122,10 +140,10 @@ struct TopList {
         n = n_;
 #pragma unroll
         for (int k = 0; k < KP; ++k) {
-            v[k] = -INFINITY;
+            v[k] = nothing<V>();
             i[k] = 0x7fffffff;
         }
-        tv = -INFINITY;
+        tv = nothing<V>();
     }
     // 32 entries in falling order, one per lane
     __device__ __forceinline__ void merge(V nv, int ni)
@@ -155,6 +173,7 @@ struct Buffer {
     uint4 ring[kAhead * 32];
     float v[kBuf];
     int i[kBuf];
+    int held;
 };
 
 template <int TYPE>
@@ -256,7 +275,7 @@ struct BeamShared {
 union WarpShared {
     Buffer buf[kBWarps];
     struct {
-        double v[kBWarps * SSQ_MAX_BEAMS];
+        long long v[kBWarps * SSQ_MAX_BEAMS];
         int i[kBWarps * SSQ_MAX_BEAMS];
     } fin;
 };
@@ -314,31 +333,34 @@ beam_kernel(const __grid_constant__ BeamCall bc)
             };
 #pragma unroll
             for (int v = 0; v < kAhead; ++v) fetch(v);
-            int held = 0;
-            auto append = [&](bool in, float f, int i) {
-                const unsigned m = __ballot_sync(0xffffffffu, in);
-                if (in) {
-                    const int to = held + __popc(m & ((1u << lane) - 1));
-                    buf.v[to] = f;
-                    buf.i[to] = i;
-                }
-                held += __popc(m);
+            if (lane == 0) buf.held = 0;
+            __syncwarp();
+            // Few lanes have anything to append, so they take their places one
+            // by one; the order does not matter, the merge sorts.
+            auto append = [&](float f, int i) {
+                const int to = atomicAdd(&buf.held, 1);
+                buf.v[to] = f;
+                buf.i[to] = i;
             };
             auto flush = [&](int least) {            // merge while `least` entries are held
                 __syncwarp();
-                while (held >= least) {
+                int held = buf.held;
+                if (held < least) return;
+                do {
                     const int e = held - 32 + lane;  // the last 32 (or fewer)
                     top.merge_any(e >= 0 ? buf.v[e] : -INFINITY,
                                   e >= 0 ? buf.i[e] : 0x7fffffff);
                     held = max(0, held - 32);
-                }
+                } while (held >= least);
+                __syncwarp();
+                if (lane == 0) buf.held = held;
                 __syncwarp();
             };
             auto edge = [&](int from, int to) {      // at most VEC - 1 logits; NaN is -inf
                 float f[1] = {-INFINITY};
                 if (from + lane < to) f[0] = fmaxf(T::one(base, from + lane), -INFINITY);
                 sum.add(f, f[0]);
-                append(f[0] > top.tv, f[0], first + from + lane);
+                if (f[0] > top.tv) append(f[0], first + from + lane);
             };
             if (head > 0) edge(0, head);
             for (int v = 0; v < blocks; ++v) {
@@ -367,13 +389,16 @@ beam_kernel(const __grid_constant__ BeamCall bc)
                     sort32(least, who);
                     least = nsel <= 32 ? __shfl_sync(0xffffffffu, least, (nsel - 1) & 31)
                                        : -INFINITY;
+                    if (mx >= least)
 #pragma unroll
-                    for (int k = 0; k < VEC; ++k)
-                        append(f[k] >= least && f[k] > -INFINITY, f[k], i0 + k);
+                        for (int k = 0; k < VEC; ++k)
+                            if (f[k] >= least && f[k] > -INFINITY) append(f[k], i0 + k);
                     flush(1);
                 } else if (__any_sync(0xffffffffu, mx > top.tv)) {
+                    if (mx > top.tv)
 #pragma unroll
-                    for (int k = 0; k < VEC; ++k) append(f[k] > top.tv, f[k], i0 + k);
+                        for (int k = 0; k < VEC; ++k)
+                            if (f[k] > top.tv) append(f[k], i0 + k);
                     flush(32);
                 }
             }
@@ -453,7 +478,7 @@ beam_kernel(const __grid_constant__ BeamCall bc)
             if (lane == 0) sh.lse[row] = done ? 0.0 : (double)m + log(s);
         }
         __syncthreads();
-        TopList<double, KP> best;
+        TopList<long long, KP> best;
         best.clear(nsel);
         for (int li = warp; li < K * CS; li += kBWarps) {
             const int q = li / K, row = li - q * K;
@@ -467,14 +492,14 @@ beam_kernel(const __grid_constant__ BeamCall bc)
                 if (32 * k >= nsel) break;
                 const bool has = e < nsel;
                 const int i = has ? oi[row * wpr * nsel + e] : 0x7fffffff;
-                double val = i == 0x7fffffff
+                const double value = i == 0x7fffffff
                     ? -INFINITY : sc + ((double)ov[row * wpr * nsel + e] - lse);
-                // NaN: a score or a row without a finite sum
-                const bool valid = val > -INFINITY;
-                if (!valid) val = -INFINITY;
+                // NaN: a score or a row without a finite sum.  (+ 0.0: no -0)
+                const bool valid = value > -INFINITY;
+                long long val = valid ? order_of(value + 0.0) : nothing<long long>();
                 int flat = valid ? row * V + i : 0x7fffffff;
                 // logits that differ may give equal values: then sort again
-                const double nv = __shfl_down_sync(0xffffffffu, val, 1);
+                const long long nv = __shfl_down_sync(0xffffffffu, val, 1);
                 const int ni = __shfl_down_sync(0xffffffffu, flat, 1);
                 if (__any_sync(0xffffffffu, lane < 31 && better(nv, ni, val, flat)))
                     sort32(val, flat);
@@ -482,7 +507,9 @@ beam_kernel(const __grid_constant__ BeamCall bc)
             }
         }
         // the warps' lists two by two
-        for (int w = kBWarps / 2; w > 0; w /= 2) {
+        int lists = kBWarps;                          // warps that have any
+        while (lists / 2 >= K * CS) lists /= 2;
+        for (int w = lists / 2; w > 0; w /= 2) {
             if (warp >= w && warp < 2 * w) {
 #pragma unroll
                 for (int k = 0; k < KP; ++k)
@@ -498,7 +525,7 @@ beam_kernel(const __grid_constant__ BeamCall bc)
                     const int e = lane + 32 * k;
                     if (32 * k >= nsel) break;
                     const bool has = e < nsel;
-                    best.merge(has ? ws.fin.v[(warp + w) * nsel + e] : -INFINITY,
+                    best.merge(has ? ws.fin.v[(warp + w) * nsel + e] : nothing<long long>(),
                                has ? ws.fin.i[(warp + w) * nsel + e] : 0x7fffffff);
                 }
             }
@@ -510,7 +537,7 @@ beam_kernel(const __grid_constant__ BeamCall bc)
                 if (e < nsel) {
                     const long long at = (long long)req * nsel + e;
                     const bool none = best.i[k] == 0x7fffffff;
-                    bc.out_score[at] = none ? -INFINITY : (float)best.v[k];
+                    bc.out_score[at] = none ? -INFINITY : (float)value_of(best.v[k]);
                     bc.out_parent[at] = none ? -1 : best.i[k] / V;
                     bc.out_token[at] = none ? -1 : best.i[k] % V;
                 }
