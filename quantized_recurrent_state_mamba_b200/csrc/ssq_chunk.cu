@@ -756,8 +756,11 @@ chunk_kernel(const __grid_constant__ PoolView pv, const __grid_constant__ Ragged
 
     // ---- one item after another: a pair of units of one segment of one run,
     // handed out in order so that blocks that finish early take more
-    for (bool armed = false;;) {
-    if (tid == 0) tl.item = atomicAdd(&rc.plan->next[STATE ? 0 : 1], 1);
+    for (bool armed = false, first = true;; first = false) {
+    // (the first item is the block's own)
+    if (tid == 0)
+        tl.item = first ? (int)blockIdx.x
+                        : (int)gridDim.x + atomicAdd(&rc.plan->next[STATE ? 0 : 1], 1);
     tc::fence_before();
     __syncthreads();
     tc::fence_after();

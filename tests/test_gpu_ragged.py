@@ -224,3 +224,321 @@ def test_chunks_segments(fmt, fresh):
     y, b, a, pool, cfg = run(ssq, i, lens, fmt, fresh=fr)
     check(i, lens, fmt, y, b, a, fresh=fr)
     assert ssq.ssq_pool_error(cfg, pool) == 0
+
+
+# ---------------------------------------------------------------------------
+# What a call may not touch, and what must not spread
+# ---------------------------------------------------------------------------
+
+def test_strides_and_alignment():
+    """Slices of one fused activation, separate tensors and a base that is not
+    16-byte aligned give the same values: bit for bit where the path is the
+    same, within the path's tolerance where the last takes the other one."""
+    ssq = require_gpu()
+    lens = [150, 3, 40]
+    i = inputs(lens, 4, 64, 128, 2, torch.bfloat16, 6)
+    y1, b1, a1, _, _ = run(ssq, i, lens, "f32")
+    j = dict(i, x=i["x"].contiguous(), B=i["B"].contiguous(), C=i["C"].contiguous(),
+             dt=torch.cat([i["dt"], i["dt"]], 1)[:, :4])
+    y2, _, a2, _, _ = run(ssq, j, lens, "f32")
+    assert torch.equal(y1, y2) and torch.equal(a1, a2)
+    total, w = sum(lens), 4 * 64 + 2 * 2 * 128
+    odd = torch.empty(total * w + 1, dtype=torch.bfloat16, device="cuda")[1:].view(total, w)
+    odd.copy_(torch.cat([i["x"].flatten(1), i["B"].flatten(1), i["C"].flatten(1)], 1))
+    k = dict(i, x=odd[:, :256].unflatten(1, (4, 64)), B=odd[:, 256:512].unflatten(1, (2, 128)),
+             C=odd[:, 512:].unflatten(1, (2, 128)))
+    y3, b3, a3, _, _ = run(ssq, k, lens, "f32")
+    check(k, lens, "f32", y3, b3, a3)
+    # y with its own stride
+    wide = torch.zeros(total, 4 * 64 + 8, dtype=torch.bfloat16, device="cuda")
+    y4, _, a4, _, _ = run(ssq, i, lens, "f32", y=wide[:, :256].unflatten(1, (4, 64)))
+    assert torch.equal(y4, y1) and torch.equal(a4, a1) and not wide[:, 256:].any()
+
+
+@pytest.mark.parametrize("n", [1, 20, 200])
+def test_leaves_the_rest_alone(n):
+    """Tokens outside every request, slots that are not named and other layers
+    keep what they hold."""
+    ssq = require_gpu()
+    H, Pd, N = 3, 64, 128
+    lens = [n, n]
+    i = inputs([5] + lens + [7], H, Pd, N, 1, torch.bfloat16, 7)
+    i["cu"] = i["cu"][1:4].contiguous()
+    i["S0"] = i["S0"][:2].contiguous()
+    total = i["x"].shape[0]
+    y = torch.full((total, H, Pd), 7.0, dtype=torch.bfloat16, device="cuda")
+    cfg = ssq.Config(3, 5, H, Pd, N, 1, "i8a")
+    pool = torch.randint(0, 255, (ssq.ssq_pool_layout(cfg)[0]["pool_bytes"],), dtype=torch.uint8,
+                         device="cuda")
+    pool[:256] = 0
+    before = pool.clone()
+    slots = torch.tensor([3, 1], dtype=torch.int32, device="cuda")
+    fresh = torch.ones(2, dtype=torch.uint8, device="cuda")
+    ws = ssq.alloc_prefill_workspace(cfg, 2, n)
+    ssq.ssq_prefill_ragged(cfg, pool, slots, 2, 1, i["cu"], n, i["x"], i["B"], i["C"], i["dt"],
+                           i["A"], i["D"], y, fresh=fresh, workspace=ws)
+    assert (y[:5] == 7).all() and (y[5 + 2 * n:] == 7).all() and not (y[5:5 + 2 * n] == 7).all()
+    L = ssq.ssq_pool_layout(cfg)[0]
+    changed = (pool != before)
+    assert not changed[:256].any()
+    body = changed[256:].view(5, L["slot_bytes"])
+    assert not body[[0, 2, 4]].any() and body[1].any() and body[3].any()
+    for off, lay in (("codes_off", "codes_layer_bytes"), ("meta_off", "meta_layer_bytes")):
+        for l in (0, 2):
+            a = L[off] + l * L[lay]
+            assert not body[:, a:a + L[lay]].any()
+
+
+@pytest.mark.parametrize("n", [6, 150])
+def test_bad_requests_are_skipped(n):
+    """A range that falls, leaves the batch or is longer than max_len, and a
+    slot outside the pool: the request is skipped and reported, the others
+    are done."""
+    ssq = require_gpu()
+    lens = [n, n, n, n]
+    i = inputs(lens, 2, 64, 128, 1, torch.bfloat16, 8)
+    good_y, _, good_a, _, _ = run(ssq, i, lens, "f32")
+    cfg = ssq.Config(1, 6, 2, 64, 128, 1, "f32")
+
+    def call(cu, slots, max_len):
+        pool = ssq.alloc_pool(cfg)
+        base = torch.tensor([4, 3, 2, 1], dtype=torch.int32, device="cuda")
+        ssq.ssq_quantize_rows(cfg, pool, base, 4, 0, 1, i["S0"])
+        y = torch.full_like(good_y, 7.0)
+        ws = ssq.alloc_prefill_workspace(cfg, 4, max_len)
+        ssq.ssq_prefill_ragged(cfg, pool, torch.tensor(slots, dtype=torch.int32, device="cuda"), 4,
+                               0, torch.tensor(cu, dtype=torch.int32, device="cuda"), max_len,
+                               i["x"], i["B"], i["C"], i["dt"], i["A"], i["D"], y, workspace=ws)
+        S = torch.empty(4, 2, 64, 128, device="cuda")
+        ssq.ssq_dequantize_rows(cfg, pool, base, 4, 0, 1, S)
+        return y, S, ssq.ssq_pool_error(cfg, pool)
+
+    cu = [0, n, 2 * n, 3 * n, 4 * n]
+    for slots in ([4, 99, 2, 1], [4, -1, 2, 1]):
+        y, S, err = call(cu, slots, n)
+        assert err == ssq.SSQ_DEVERR_SLOT
+        assert (y[n:2 * n] == 7).all() and torch.equal(S[1], i["S0"][1])
+        assert torch.equal(y[2 * n:], good_y[2 * n:]) and torch.equal(S[2:], good_a[2:])
+    for bad, skipped in (([0, n, 2 * n, 3 * n, 4 * n + 1], [3]),          # past the batch
+                         ([-1, n, 2 * n, 3 * n, 4 * n], [0]),
+                         ([0, n, n - 1, 3 * n, 4 * n], [1, 2])):          # falls, then too long
+        y, S, err = call(bad, [4, 3, 2, 1], n)
+        assert err == ssq.SSQ_DEVERR_TOKENS
+        for b in range(4):
+            if b in skipped:
+                assert torch.equal(S[b], i["S0"][b])
+            else:
+                assert torch.equal(S[b], good_a[b])
+    y, S, err = call(cu, [4, 3, 2, 1], n - 1)                             # all longer than max_len
+    assert err == ssq.SSQ_DEVERR_TOKENS and (y == 7).all() and torch.equal(S, i["S0"])
+
+
+@pytest.mark.parametrize("dtype,n", [(torch.bfloat16, 200), (torch.float16, 30)])
+@pytest.mark.parametrize("what,value", [("x", math.nan), ("x", math.inf), ("B", math.nan),
+                                        ("C", math.inf), ("dt", math.nan)])
+def test_non_finite_stays_where_it_is(dtype, n, what, value):
+    """A non-finite value at one token of one request reaches its own and later
+    tokens of that request only (x: of its row only; C: of its token only),
+    not its earlier tokens in the same chunk and not the neighbours in the
+    packed batch."""
+    ssq = require_gpu()
+    H, Pd, N = 2, 64, 128
+    lens = [n, n, n]
+    at = n + n // 2                                   # a token of the middle request
+    i = inputs(lens, H, Pd, N, 1, dtype, 9)
+    y0, _, a0, _, _ = run(ssq, i, lens, "f32")
+    if what == "x":
+        i["x"][at, 1, 5] = value
+    elif what == "dt":
+        i["dt"][at, 1] = value
+    else:
+        i[what][at, 0, 3] = value
+    y, _, a, pool, cfg = run(ssq, i, lens, "f32")
+    hit = torch.zeros_like(y0, dtype=torch.bool)      # what may change
+    if what == "x":
+        hit[at:2 * n, 1, 5] = True
+    elif what == "dt":
+        hit[at:2 * n, 1] = True
+    elif what == "B":
+        hit[at:2 * n] = True
+    else:
+        hit[at] = True
+    assert torch.equal(y[~hit], y0[~hit])
+    assert not y[hit].isfinite().any()
+    same = torch.ones_like(a0, dtype=torch.bool)
+    if what == "x":
+        same[1, 1, 5] = False
+    elif what == "dt":
+        same[1, 1] = False
+    elif what == "B":
+        same[1] = False
+    assert torch.equal(a[same], a0[same])
+    if what in ("x", "dt"):
+        assert not a[~same].isfinite().any()
+
+
+@pytest.mark.parametrize("n", [5, 140])
+def test_non_finite_row_is_reported(n):
+    """A quantized row that is not finite at the end sets the pool's bit."""
+    ssq = require_gpu()
+    i = inputs([n], 2, 64, 128, 1, torch.bfloat16, 10)
+    i["x"][n - 1, 0, 3] = math.nan
+    y, _, a, pool, cfg = run(ssq, i, [n], "i8a")
+    assert ssq.ssq_pool_error(cfg, pool) == ssq.SSQ_DEVERR_NONFINITE
+    assert a[0, 0, 3].isnan().all()
+    a[0, 0, 3] = 0
+    assert a.isfinite().all()
+
+
+def test_decay_extremes():
+    """Steps that forget everything (A = -inf, large dt), steps of zero (the
+    state unchanged), and growth (A > 0) in one chunked run."""
+    ssq = require_gpu()
+    lens = [160]
+    i = inputs(lens, 4, 64, 128, 1, torch.bfloat16, 11)
+    i["A"] = torch.tensor([-math.inf, -1e6, 1e-3, -2.0], device="cuda")
+    i["dt"][:, 3] = 0.0
+    i["dt"][7, 3] = 30.0
+    y, b, a, pool, cfg = run(ssq, i, lens, "f32")
+    check(i, lens, "f32", y, b, a)
+
+
+def test_masked_heads():
+    """Heads whose mask is 0 keep fp32 rows beside quantized ones."""
+    ssq = require_gpu()
+    for n, mask in ((3, [1, 0, 1, 0]), (100, [0, 1, 1, 0])):
+        lens = [n, n + 1]
+        i = inputs(lens, 4, 40, 64, 2, torch.bfloat16, 12)
+        y, b, a, pool, cfg = run(ssq, i, lens, "i4a", mask=mask)
+        check(i, lens, "i4a", y, b, a, mask=mask)
+
+
+def test_equals_ssq_prefill_bit_for_bit():
+    """fp32 activations: the stored codes and metadata are those of ssq_prefill
+    (the same operations in the same order)."""
+    ssq = require_gpu()
+    H, Pd, N, T = 3, 12, 64, 70
+    i = inputs([T, T], H, Pd, N, 1, torch.float32, 13, fused=False)
+    for fmt in FMTS:
+        _, _, _, pool, cfg = run(ssq, i, [T, T], fmt)
+        slots = torch.tensor([2, 1], dtype=torch.int32, device="cuda")
+        other = ssq.alloc_pool(cfg)
+        ssq.ssq_quantize_rows(cfg, other, slots, 2, 0, 1, i["S0"])
+        y = torch.empty(2, T, H, Pd, device="cuda")
+        ssq.ssq_prefill(cfg, other, slots, 2, 0, T, i["x"], i["B"], i["C"], i["dt"], i["A"],
+                        i["D"], y)
+        assert torch.equal(pool, other), fmt
+
+
+def test_pieces_equal_the_whole():
+    """A prompt in pieces (an fp32 pool carries the state exactly) against the
+    same prompt in one call: both within the chunk path's tolerance of the
+    recurrence, whichever path each piece takes."""
+    ssq = require_gpu()
+    H, Pd, N, T = 2, 64, 128, 389
+    i = inputs([T], H, Pd, N, 1, torch.bfloat16, 14)
+    cfg = ssq.Config(1, 1, H, Pd, N, 1, "f32")
+    pool = ssq.alloc_pool(cfg)
+    ssq.ssq_quantize_rows(cfg, pool, None, 1, 0, 1, i["S0"])
+    y = torch.empty(T, H, Pd, dtype=torch.bfloat16, device="cuda")
+    ws = ssq.alloc_prefill_workspace(cfg, 1, T)
+    at = 0
+    for n in (128, 1, 31, 130, 64, 1, 34):
+        cu = torch.tensor([at, at + n], dtype=torch.int32, device="cuda")
+        ssq.ssq_prefill_ragged(cfg, pool, None, 1, 0, cu, n, i["x"], i["B"], i["C"], i["dt"],
+                               i["A"], i["D"], y, workspace=ws)
+        at += n
+    assert at == T
+    a = torch.empty(1, H, Pd, N, device="cuda")
+    ssq.ssq_dequantize_rows(cfg, pool, None, 1, 0, 1, a)
+    check(i, [T], "f32", y, i["S0"], a)
+
+
+# ---------------------------------------------------------------------------
+# Streams, graphs, repetition
+# ---------------------------------------------------------------------------
+
+def test_streams_and_repetition():
+    """Two calls at once on two streams, each with its slots and workspace, and
+    the same call again: the same bits every time."""
+    ssq = require_gpu()
+    lens = [1500, 9, 1, 77]
+    i = inputs(lens, 2, 64, 128, 1, torch.bfloat16, 15)
+    cfg = ssq.Config(1, 8, 2, 64, 128, 1, "i8a")
+    want = None
+    for _ in range(3):
+        pool = ssq.alloc_pool(cfg)
+        halves = []
+        torch.cuda.synchronize()
+        for k in range(2):
+            st = torch.cuda.Stream()
+            slots = torch.arange(4, dtype=torch.int32, device="cuda") + 4 * k
+            ws = ssq.alloc_prefill_workspace(cfg, 4, 1500)
+            y = torch.empty_like(i["x"], memory_format=torch.contiguous_format)
+            halves.append((st, slots, ws, y))
+        torch.cuda.synchronize()
+        for st, slots, ws, y in halves:
+            with torch.cuda.stream(st):
+                ssq.ssq_prefill_ragged(cfg, pool, slots, 4, 0, i["cu"], 1500, i["x"], i["B"],
+                                       i["C"], i["dt"], i["A"], i["D"], y, workspace=ws)
+        torch.cuda.synchronize()
+        assert torch.equal(halves[0][3], halves[1][3])
+        body = pool[256:].view(8, -1)
+        assert torch.equal(body[:4], body[4:])
+        if want is None:
+            want = (halves[0][3].clone(), pool.clone())
+        assert torch.equal(halves[0][3], want[0]) and torch.equal(pool, want[1])
+
+
+def test_captured_call_follows_its_inputs():
+    """A captured call replayed with other tokens, lengths and slots (within
+    max_len) does what an eager call on them does."""
+    ssq = require_gpu()
+    H, Pd, N = 3, 64, 128
+    first, second = [700, 1, 20, 300], [1, 640, 100, 280]
+    i, j = (inputs(l, H, Pd, N, 1, torch.bfloat16, s) for l, s in ((first, 16), (second, 17)))
+    cfg = ssq.Config(1, 4, H, Pd, N, 1, "bf16")
+    buf = {k: torch.empty_like(i[k], memory_format=torch.contiguous_format) for k in
+           ("x", "B", "C", "dt", "A", "D", "cu")}
+    slots = torch.arange(4, dtype=torch.int32, device="cuda")
+    ws = ssq.alloc_prefill_workspace(cfg, 4, 700)
+    fresh = torch.zeros(4, dtype=torch.uint8, device="cuda")
+    pool = ssq.alloc_pool(cfg)
+    y = torch.empty(sum(first), H, Pd, dtype=torch.bfloat16, device="cuda")
+
+    def call():
+        ssq.ssq_prefill_ragged(cfg, pool, slots, 4, 0, buf["cu"], 700, buf["x"], buf["B"],
+                               buf["C"], buf["dt"], buf["A"], buf["D"], y, fresh=fresh, workspace=ws)
+
+    for k in buf:
+        buf[k].copy_(i[k])
+    call()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        call()
+    for data, order in ((i, [0, 1, 2, 3]), (j, [2, 0, 3, 1]), (i, [3, 2, 1, 0])):
+        for k in buf:
+            buf[k].copy_(data[k])
+        slots.copy_(torch.tensor(order, dtype=torch.int32))
+        fresh.copy_(torch.tensor([1, 0, 1, 0], dtype=torch.uint8))
+        start = pool.clone()
+        call()
+        want_y, want = y.clone(), pool.clone()
+        pool.copy_(start)
+        y.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y, want_y) and torch.equal(pool, want)
+    del g
+
+
+def test_many_requests():
+    """More requests than a block has threads, of every kind, in one call."""
+    ssq = require_gpu()
+    lens = [1, 0, 3, 40] * 150
+    i = inputs(lens, 1, 16, 16, 1, torch.bfloat16, 18)
+    fresh = (torch.arange(600, device="cuda") % 5 == 1).to(torch.uint8)
+    y, b, a, pool, cfg = run(ssq, i, lens, "f32", fresh=fresh)
+    check(i, lens, "f32", y, b, a, fresh=fresh)
+    assert ssq.ssq_pool_error(cfg, pool) == 0
