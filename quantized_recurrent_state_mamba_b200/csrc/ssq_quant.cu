@@ -36,7 +36,7 @@ __device__ __forceinline__ QTile make_qtile(const PoolView& pv, const CallView& 
     return tl;
 }
 
-template <int FMT, int N, bool kQuantize>
+template <int FMT, int N>
 __global__ void __launch_bounds__(kThreads)
 rows_kernel(const __grid_constant__ PoolView pv, const __grid_constant__ CallView cv)
 {
@@ -79,40 +79,21 @@ rows_kernel(const __grid_constant__ PoolView pv, const __grid_constant__ CallVie
                             + (long long)rr * F::meta_bytes;
             float s[E];
             Chunk<CB> c;
-            if constexpr (kQuantize) {
-                load_f32<E>(s, cv.S_in + srow);
-                const RowParams rp = refit_row<FMT, E, LPR>(s);
-                float rq[E];
-                uint32_t k[E];
-                round_row<FMT, E>(rp, s, rq, k);
-                pack_codes<FMT, E>(k, c);
-                if (active) {
-                    store_chunk<CB>(crow, c);
-                    if (j == 0) {
-                        if constexpr (F::sym) {
-                            *reinterpret_cast<float*>(mrow) = rp.delta;
-                        } else {
-                            *reinterpret_cast<float2*>(mrow) = make_float2(rp.delta, rp.z);
-                        }
-                        if (!rp.finite) atomicOr(err, SSQ_DEVERR_NONFINITE);
+            load_f32<E>(s, cv.S_in + srow);
+            const RowParams rp = refit_row<FMT, E, LPR>(s);
+            float rq[E];
+            uint32_t k[E];
+            round_row<FMT, E>(rp, s, rq, k);
+            pack_codes<FMT, E>(k, c);
+            if (active) {
+                store_chunk<CB>(crow, c);
+                if (j == 0) {
+                    if constexpr (F::sym) {
+                        *reinterpret_cast<float*>(mrow) = rp.delta;
+                    } else {
+                        *reinterpret_cast<float2*>(mrow) = make_float2(rp.delta, rp.z);
                     }
-                }
-            } else {
-                load_chunk<CB>(c, crow);
-                float delta0, z0 = 0.0f;
-                if constexpr (F::sym) {
-                    delta0 = *reinterpret_cast<const float*>(mrow);
-                } else {
-                    const float2 m = *reinterpret_cast<const float2*>(mrow);
-                    delta0 = m.x;
-                    z0 = m.y;
-                }
-                decode_row<FMT, E>(c, delta0, z0, s);
-                if (active) {
-#pragma unroll
-                    for (int i = 0; i < E / 4; ++i)
-                        reinterpret_cast<float4*>(cv.S_out + srow)[i] =
-                            make_float4(s[4 * i], s[4 * i + 1], s[4 * i + 2], s[4 * i + 3]);
+                    if (!rp.finite) atomicOr(err, SSQ_DEVERR_NONFINITE);
                 }
             }
           }
@@ -122,77 +103,145 @@ rows_kernel(const __grid_constant__ PoolView pv, const __grid_constant__ CallVie
             uint8_t* frow = slot_base + pv.fp_off + (long long)layer * pv.fp_layer_bytes
                             + ((long long)rr * N + j * E) * EB;
             float s[E];
-            if constexpr (kQuantize) {
-                load_f32<E>(s, cv.S_in + srow);
-                if constexpr (kBf16) {
-                    Chunk<E * 2> c;
+            load_f32<E>(s, cv.S_in + srow);
+            if constexpr (kBf16) {
+                Chunk<E * 2> c;
 #pragma unroll
-                    for (int n = 0; n < E; n += 2) {
-                        c.w[n / 2] = (uint32_t)__bfloat16_as_ushort(__float2bfloat16_rn(s[n]))
-                                     | ((uint32_t)__bfloat16_as_ushort(__float2bfloat16_rn(s[n + 1])) << 16);
-                    }
-                    store_chunk<E * 2>(frow, c);
-                } else {
-                    Chunk<E * 4> c;
-#pragma unroll
-                    for (int n = 0; n < E; ++n) c.w[n] = __float_as_uint(s[n]);
-                    store_chunk<E * 4>(frow, c);
+                for (int n = 0; n < E; n += 2) {
+                    c.w[n / 2] = (uint32_t)__bfloat16_as_ushort(__float2bfloat16_rn(s[n]))
+                                 | ((uint32_t)__bfloat16_as_ushort(__float2bfloat16_rn(s[n + 1])) << 16);
                 }
+                store_chunk<E * 2>(frow, c);
             } else {
-                if constexpr (kBf16) {
-                    Chunk<E * 2> c;
-                    load_chunk<E * 2>(c, frow);
+                Chunk<E * 4> c;
 #pragma unroll
-                    for (int n = 0; n < E; ++n)
-                        s[n] = __uint_as_float((c.w[n / 2] >> (16 * (n % 2))) << 16);
-                } else {
-                    Chunk<E * 4> c;
-                    load_chunk<E * 4>(c, frow);
-#pragma unroll
-                    for (int n = 0; n < E; ++n) s[n] = __uint_as_float(c.w[n]);
-                }
-#pragma unroll
-                for (int i = 0; i < E / 4; ++i)
-                    reinterpret_cast<float4*>(cv.S_out + srow)[i] =
-                        make_float4(s[4 * i], s[4 * i + 1], s[4 * i + 2], s[4 * i + 3]);
+                for (int n = 0; n < E; ++n) c.w[n] = __float_as_uint(s[n]);
+                store_chunk<E * 4>(frow, c);
             }
         }
     }
 }
 
-template <int FMT, int N, bool Q>
+// Decoding has no row-wide step, so a thread takes the entries of one 4-byte
+// word of codes (fp rows: 4 entries) of a row: loads and stores of a warp are
+// whole lines.  (With the rows' lanes each holding 32 consecutive entries,
+// 256 slots of 32 heads x 128 x 128 int8 took 219 us.)
+template <int FMT>
+__global__ void __launch_bounds__(kThreads)
+dequant_kernel(const __grid_constant__ PoolView pv, const __grid_constant__ CallView cv)
+{
+    using F = Fmt<FMT>;
+    constexpr bool kBf16 = (FMT == SSQ_BF16);
+    constexpr int QE = F::quant ? 32 / F::bits : 4;      // entries of a thread in a quantized row
+    constexpr uint32_t kMask = F::quant ? (1u << F::bits % 32) - 1 : 0;
+    const int N = pv.N, P = pv.P, H = pv.H;
+    const int shift = __ffs(N / 4) - 1;                   // N is a power of two
+    const int words = (H * P) << shift;                   // of a (layer, request)
+    for (long long lb = blockIdx.y; lb < (long long)cv.nl * cv.batch; lb += gridDim.y) {
+        const int l = (int)(lb / cv.batch), b = (int)(lb - (long long)l * cv.batch);
+        const int slot = cv.slot_idx ? __ldg(cv.slot_idx + b) : b;
+        if (slot < 0 || slot >= pv.n_slots) {
+            if (blockIdx.x == 0 && threadIdx.x == 0)
+                atomicOr(reinterpret_cast<uint32_t*>(pv.pool), SSQ_DEVERR_SLOT);
+            continue;
+        }
+        const int layer = cv.layer0 + l;
+        const uint8_t* base = pv.pool + pv.header_bytes + (long long)slot * pv.slot_bytes;
+        for (int i = blockIdx.x * kThreads + threadIdx.x; i < words; i += gridDim.x * kThreads) {
+            const int rr = i >> shift, n4 = i & (N / 4 - 1);
+            const int hp = fdiv(rr, pv.mP), p = rr - hp * P;
+            const bool quant = F::quant && hp < pv.Hq;
+            const int h = pv.perm[hp];
+            float* out = cv.S_out + ((lb * H + h) * P + p) * N;
+            if (F::quant && quant) {
+                if (n4 >= N / QE) continue;              // 4-bit rows have half the words
+                const long long row = (long long)hp * P + p;
+                const uint32_t c = __ldcs(reinterpret_cast<const uint32_t*>(
+                    base + pv.codes_off + (long long)layer * pv.codes_layer_bytes
+                    + row * (N * F::bits / 8)) + n4);
+                const uint8_t* m = base + pv.meta_off + (long long)layer * pv.meta_layer_bytes
+                                   + row * F::meta_bytes;
+                float delta, z = 0.0f;
+                if constexpr (F::sym) {
+                    delta = __ldg(reinterpret_cast<const float*>(m));
+                } else {
+                    const float2 t = __ldg(reinterpret_cast<const float2*>(m));
+                    delta = t.x;
+                    z = t.y;
+                }
+                float v[QE];
+#pragma unroll
+                for (int k = 0; k < QE; ++k) {
+                    const uint32_t u = (c >> (F::bits * k)) & kMask;
+                    const int q = F::sym ? (int)(u << (32 - F::bits)) >> (32 - F::bits) : (int)u;
+                    v[k] = __fmul_rn(__fsub_rn((float)q, z), delta);
+                }
+#pragma unroll
+                for (int k = 0; k < QE; k += 4)
+                    __stcs(reinterpret_cast<float4*>(out + n4 * QE + k),
+                           make_float4(v[k], v[k + 1], v[k + 2], v[k + 3]));
+            } else {
+                const long long row = (long long)(hp - pv.Hq) * P + p;
+                const uint8_t* f = base + pv.fp_off + (long long)layer * pv.fp_layer_bytes;
+                float4 v;
+                if constexpr (kBf16) {
+                    const uint2 w = __ldcs(reinterpret_cast<const uint2*>(f + row * N * 2) + n4);
+                    v = make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u),
+                                    __uint_as_float(w.y << 16), __uint_as_float(w.y & 0xffff0000u));
+                } else {
+                    v = __ldcs(reinterpret_cast<const float4*>(f + row * N * 4) + n4);
+                }
+                __stcs(reinterpret_cast<float4*>(out) + n4, v);
+            }
+        }
+    }
+}
+
+template <int FMT>
+cudaError_t launch_dequant_fmt(const PoolView& pv, const CallView& cv, cudaStream_t st)
+{
+    const long long lb = (long long)cv.nl * cv.batch;
+    const long long words = (long long)pv.H * pv.P * (pv.N / 4);
+    // several words a thread where there are enough (layer, request) pairs
+    long long gx = (words + 4 * kThreads - 1) / (4 * kThreads);
+    const long long gy = lb < 65535 ? lb : 65535;
+    if (gx > 4096) gx = 4096;
+    dequant_kernel<FMT><<<dim3((unsigned)gx, (unsigned)gy), kThreads, 0, st>>>(pv, cv);
+    return cudaGetLastError();
+}
+
+template <int FMT, int N>
 cudaError_t launch_rows_n(const PoolView& pv, const CallView& cv, cudaStream_t st)
 {
-    auto kern = rows_kernel<FMT, N, Q>;
+    auto kern = rows_kernel<FMT, N>;
     const int grid = grid_for((const void*)kern, kThreads, cv.total_tiles);
     if (grid <= 0) return cudaErrorInvalidConfiguration;
     kern<<<grid, kThreads, 0, st>>>(pv, cv);
     return cudaGetLastError();
 }
 
-template <int FMT, bool Q>
+template <int FMT>
 cudaError_t launch_rows_fmt(const PoolView& pv, const CallView& cv, cudaStream_t st)
 {
     switch (pv.N) {
-    case 16: return launch_rows_n<FMT, 16, Q>(pv, cv, st);
-    case 32: return launch_rows_n<FMT, 32, Q>(pv, cv, st);
-    case 64: return launch_rows_n<FMT, 64, Q>(pv, cv, st);
-    case 128: return launch_rows_n<FMT, 128, Q>(pv, cv, st);
-    case 256: return launch_rows_n<FMT, 256, Q>(pv, cv, st);
+    case 16: return launch_rows_n<FMT, 16>(pv, cv, st);
+    case 32: return launch_rows_n<FMT, 32>(pv, cv, st);
+    case 64: return launch_rows_n<FMT, 64>(pv, cv, st);
+    case 128: return launch_rows_n<FMT, 128>(pv, cv, st);
+    case 256: return launch_rows_n<FMT, 256>(pv, cv, st);
     default: return cudaErrorInvalidValue;
     }
 }
 
-template <bool Q>
 cudaError_t launch_rows(const PoolView& pv, const CallView& cv, int fmt, cudaStream_t st)
 {
     switch (fmt) {
-    case SSQ_F32: return launch_rows_fmt<SSQ_F32, Q>(pv, cv, st);
-    case SSQ_BF16: return launch_rows_fmt<SSQ_BF16, Q>(pv, cv, st);
-    case SSQ_I8_SYM: return launch_rows_fmt<SSQ_I8_SYM, Q>(pv, cv, st);
-    case SSQ_I8_ASYM: return launch_rows_fmt<SSQ_I8_ASYM, Q>(pv, cv, st);
-    case SSQ_I4_SYM: return launch_rows_fmt<SSQ_I4_SYM, Q>(pv, cv, st);
-    case SSQ_I4_ASYM: return launch_rows_fmt<SSQ_I4_ASYM, Q>(pv, cv, st);
+    case SSQ_F32: return launch_rows_fmt<SSQ_F32>(pv, cv, st);
+    case SSQ_BF16: return launch_rows_fmt<SSQ_BF16>(pv, cv, st);
+    case SSQ_I8_SYM: return launch_rows_fmt<SSQ_I8_SYM>(pv, cv, st);
+    case SSQ_I8_ASYM: return launch_rows_fmt<SSQ_I8_ASYM>(pv, cv, st);
+    case SSQ_I4_SYM: return launch_rows_fmt<SSQ_I4_SYM>(pv, cv, st);
+    case SSQ_I4_ASYM: return launch_rows_fmt<SSQ_I4_ASYM>(pv, cv, st);
     default: return cudaErrorInvalidValue;
     }
 }
@@ -202,13 +251,21 @@ cudaError_t launch_rows(const PoolView& pv, const CallView& cv, int fmt, cudaStr
 cudaError_t launch_quantize(const PoolView& pv, const CallView& cv, int fmt,
                             cudaStream_t st)
 {
-    return launch_rows<true>(pv, cv, fmt, st);
+    return launch_rows(pv, cv, fmt, st);
 }
 
 cudaError_t launch_dequantize(const PoolView& pv, const CallView& cv, int fmt,
                               cudaStream_t st)
 {
-    return launch_rows<false>(pv, cv, fmt, st);
+    switch (fmt) {
+    case SSQ_F32: return launch_dequant_fmt<SSQ_F32>(pv, cv, st);
+    case SSQ_BF16: return launch_dequant_fmt<SSQ_BF16>(pv, cv, st);
+    case SSQ_I8_SYM: return launch_dequant_fmt<SSQ_I8_SYM>(pv, cv, st);
+    case SSQ_I8_ASYM: return launch_dequant_fmt<SSQ_I8_ASYM>(pv, cv, st);
+    case SSQ_I4_SYM: return launch_dequant_fmt<SSQ_I4_SYM>(pv, cv, st);
+    case SSQ_I4_ASYM: return launch_dequant_fmt<SSQ_I4_ASYM>(pv, cv, st);
+    default: return cudaErrorInvalidValue;
+    }
 }
 
 }  // namespace ssq
