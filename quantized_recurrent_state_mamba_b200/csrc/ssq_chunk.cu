@@ -747,8 +747,8 @@ chunk_kernel(const __grid_constant__ PoolView pv, const __grid_constant__ Ragged
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
     const int tiles = (pv.P + kPT - 1) / kPT;
-    const int per_group = pv.hpg * tiles, pairs_group = (per_group + 1) / 2;
-    const int pairs = pairs_group * pv.G;
+    const int per_group = pv.hpg * tiles, upb = rc.units_per_block;
+    const int pairs_group = (per_group + upb - 1) / upb, pairs = pairs_group * pv.G;
     const int halves = pv.N > 64 ? 2 : 1;           // 64-column halves of C and B
     if (tid == 0) tl.dead = 0;
     if (warp == kElemWarps + 1) tc::alloc(&tl.tmem, kTmemCols);
@@ -773,8 +773,8 @@ chunk_kernel(const __grid_constant__ PoolView pv, const __grid_constant__ Ragged
         wk.b = at.x;
         wk.seg = at.y;
         wk.g = pr / pairs_group;
-        const int u0 = (pr - wk.g * pairs_group) * 2;
-        wk.nu = min(2, per_group - u0);
+        const int u0 = (pr - wk.g * pairs_group) * upb;
+        wk.nu = min(upb, per_group - u0);
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
             const int uu = min(u0 + u, per_group - 1);
@@ -1095,10 +1095,11 @@ cudaError_t make_map(CUtensorMap* map, const void* base, int inner, int mid, lon
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-int chunk_pairs(int H, int P, int G)
+// Blocks' worth of units of a request.
+long long chunk_items(int H, int P, int G, int units_per_block)
 {
     const int per_group = H / G * ((P + kPT - 1) / kPT);
-    return (per_group + 1) / 2 * G;
+    return (long long)((per_group + units_per_block - 1) / units_per_block) * G;
 }
 
 template <bool STATE>
@@ -1108,7 +1109,7 @@ cudaError_t launch_pass(const PoolView& pv, const RaggedCall& rc, const ChunkMap
     thread_local int done = -1;
     cudaError_t e = allow_smem(chunk_kernel<STATE>, kSmemBytes, &done);
     if (e != cudaSuccess) return e;
-    const long long items = (long long)chunk_pairs(pv.H, pv.P, pv.G) * rc.batch * rc.nseg;
+    const long long items = chunk_items(pv.H, pv.P, pv.G, rc.units_per_block) * rc.batch * rc.nseg;
     if (items > 0x3fffffffLL) return cudaErrorInvalidConfiguration;
     const unsigned blocks = (unsigned)(items < kSMs ? items : kSMs);
     chunk_kernel<STATE><<<blocks, kCThreadsTotal, kSmemBytes, st>>>(pv, rc, maps, fmt);
@@ -1117,18 +1118,28 @@ cudaError_t launch_pass(const PoolView& pv, const RaggedCall& rc, const ChunkMap
 
 }  // namespace
 
-void chunk_plan(int H, int P, int G, int batch, int max_len, int* nseg, int* seg_chunks)
+void chunk_plan(int H, int P, int G, int batch, int max_len, ChunkShape* cs)
 {
-    *nseg = 1;
-    *seg_chunks = 0x7fffffff / kL;                  // a run is one segment
+    cs->nseg = 1;
+    cs->seg_chunks = 0x7fffffff / kL;               // a run is one segment
+    cs->units_per_block = 2;
     if (batch < 1) return;
+    // A block with one unit takes 6000 cycles a chunk, with two 7700: one each
+    // where every unit gets an SM of its own.
     const int chunks = (int)(((long long)max_len + kL - 1) / kL);
-    const long long blocks = (long long)chunk_pairs(H, P, G) * batch;
-    const long long fit = kSMs / blocks;
-    long long n = chunks / 4 < fit ? chunks / 4 : fit;
+    if (chunk_items(H, P, G, 1) * batch <= kSMs) cs->units_per_block = 1;
+    // Segments of four chunks or more, while they fit the SMs at once: the
+    // first pass costs about half a main pass again.
+    const long long fit = kSMs / (chunk_items(H, P, G, cs->units_per_block) * batch);
+    const long long n = chunks / 4 < fit ? chunks / 4 : fit;
     if (n < 2) return;
-    *seg_chunks = (int)((chunks + n - 1) / n);
-    *nseg = (chunks + *seg_chunks - 1) / *seg_chunks;
+    // with segments every SM is busy: two units a block
+    const long long fit2 = kSMs / (chunk_items(H, P, G, 2) * batch);
+    const long long n2 = chunks / 4 < fit2 ? chunks / 4 : fit2;
+    if (n2 > n) cs->units_per_block = 2;
+    const long long m = n2 > n ? n2 : n;
+    cs->seg_chunks = (int)((chunks + m - 1) / m);
+    cs->nseg = (chunks + cs->seg_chunks - 1) / cs->seg_chunks;
 }
 
 cudaError_t launch_ragged_chunks(const PoolView& pv, const RaggedCall& rc, int fmt,

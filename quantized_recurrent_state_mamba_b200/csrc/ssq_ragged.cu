@@ -44,57 +44,35 @@ __device__ __forceinline__ void store_act(void* p, long long i, float v)
         reinterpret_cast<float*>(p)[i] = v;
 }
 
-// E consecutive activations as fp32 pairs, in pieces as wide as the address
-// allows.
-template <int TYPE, int E>
-__device__ __forceinline__ void load_acts(const void* p, long long i, float2 (&v)[E / 2])
-{
-    constexpr int EB = TYPE == SSQ_T_F32 ? 4 : 2, WB = E * EB < 16 ? E * EB : 16;
-    constexpr int WORDS = E * EB / 4;
-    static_assert(WB == 8 || WB == 16, "");
-    const char* a = reinterpret_cast<const char*>(p) + i * EB;
-    if ((reinterpret_cast<uintptr_t>(a) & (WB - 1)) == 0) {
-        uint32_t u[WORDS];
-#pragma unroll
-        for (int k = 0; k < WORDS; k += WB / 4) {
-            if constexpr (WB == 16) {
-                const uint4 w = __ldg(reinterpret_cast<const uint4*>(a + k * 4));
-                u[k] = w.x; u[k + 1] = w.y; u[k + 2] = w.z; u[k + 3] = w.w;
-            } else {
-                const uint2 w = __ldg(reinterpret_cast<const uint2*>(a + k * 4));
-                u[k] = w.x; u[k + 1] = w.y;
-            }
-        }
-#pragma unroll
-        for (int k = 0; k < E / 2; ++k) {
-            if constexpr (TYPE == SSQ_T_F32)
-                v[k] = make_float2(__uint_as_float(u[2 * k]), __uint_as_float(u[2 * k + 1]));
-            else if constexpr (TYPE == SSQ_T_BF16)
-                v[k] = make_float2(__uint_as_float(u[k] << 16),
-                                   __uint_as_float(u[k] & 0xffff0000u));
-            else
-                v[k] = __half22float2(*reinterpret_cast<const __half2*>(&u[k]));
-        }
-    } else {
-#pragma unroll
-        for (int k = 0; k < E; k += 2)
-            v[k / 2] = make_float2(load_act<TYPE>(p, i + k), load_act<TYPE>(p, i + k + 1));
-    }
-}
-
 // Floats of one staged row of B or C: LPR pieces of E floats, 4 floats apart.
 template <int N>
 constexpr int kRowF = Shape<N>::LPR * (Shape<N>::E + 4);
 
+// Where entry n of B or C is staged: lane by lane, in the order in which a
+// lane holds the entries of its row.
+template <int RF, int N>
+__device__ __forceinline__ int staged_row(int n)
+{
+    constexpr int E = Shape<N>::E, LPR = Shape<N>::LPR, PE = kPiece<RF, N>;
+    const int piece = n / PE;
+    return (piece % LPR) * (E + 4) + piece / LPR * PE + n % PE;
+}
+template <int FMT, int N>
+__device__ __forceinline__ int staged_at(bool quant, int n)
+{
+    return !Fmt<FMT>::quant || quant ? staged_row<FMT, N>(n) : staged_row<SSQ_F32, N>(n);
+}
+
 // ---- single tokens --------------------------------------------------------
 // One warp takes `steps` groups of RPW = 32/LPR rows of one head of one request
-// and loads a group's rows while it works on the one before.  No shared memory, no barrier: what bounds it
-// is the pool's traffic (fp rows) or the issue of the refit and rounding
-// (integer rows).
+// and loads a group's rows while it works on the one before.  B and C lie in the
+// warp's own piece of shared memory in fp32 (unpacking them for every group of
+// rows took a fifth of the instructions).  What bounds it is the pool's traffic
+// (fp rows) or the issue of the refit and rounding (integer rows).
 template <int RF, int N, int TYPE>
 __device__ __forceinline__ void single_unit(const PoolView& pv, const RaggedCall& rc,
                                             const Run& run, const RowPlace& place, int h, int p0,
-                                            int steps)
+                                            int steps, float* sB, float* sC)
 {
     constexpr int E = Shape<N>::E, LPR = Shape<N>::LPR, RPW = Shape<N>::RPW;
     const int lane = threadIdx.x & 31, j = lane % LPR;
@@ -106,8 +84,16 @@ __device__ __forceinline__ void single_unit(const PoolView& pv, const RaggedCall
     const long long xat = t * rc.xs + (long long)h * pv.P;
     float xn = p < pv.P ? load_act<TYPE>(rc.x, xat + p) : 0.0f;
     const float dt = __ldg(rc.dt + t * rc.dts + h);
-    constexpr int PE = kPiece<RF, N> < 16 ? kPiece<RF, N> : 16;
-    const long long Bat = t * rc.Bs + (long long)g * N, Cat = t * rc.Cs + (long long)g * N;
+    __syncwarp();                                    // the unit before is done with them
+#pragma unroll
+    for (int n = lane; n < N; n += 32) {
+        const int at = staged_row<RF, N>(n);
+        sB[at] = load_act<TYPE>(rc.B, t * rc.Bs + (long long)g * N + n);
+        sC[at] = load_act<TYPE>(rc.C, t * rc.Cs + (long long)g * N + n);
+    }
+    __syncwarp();
+    const float4* Bp = reinterpret_cast<const float4*>(sB + j * (E + 4));
+    const float4* Cp = reinterpret_cast<const float4*>(sC + j * (E + 4));
     const float lam = decay(dt, __ldg(rc.A + h)), D = __ldg(rc.D + h);
     const float2 l2 = make_float2(lam, lam);
     for (int k = 0; k < steps; ++k) {
@@ -123,17 +109,14 @@ __device__ __forceinline__ void single_unit(const PoolView& pv, const RaggedCall
         const float2 x2 = make_float2(dtx, dtx);
         float2 acc = make_float2(0.0f, 0.0f);
 #pragma unroll
-        for (int q = 0; q < E; q += PE) {            // B and C again from L1
-            float2 Bv[PE / 2], Cv[PE / 2];
-            load_acts<TYPE, PE>(rc.B, Bat + row_entry<RF, N>(q, j), Bv);
-            load_acts<TYPE, PE>(rc.C, Cat + row_entry<RF, N>(q, j), Cv);
-#pragma unroll
-            for (int n = 0; n < PE; n += 2) {
-                const float2 v = fma2(l2, make_float2(s[q + n], s[q + n + 1]), mul2(x2, Bv[n / 2]));
-                s[q + n] = v.x;
-                s[q + n + 1] = v.y;
-                acc = fma2(Cv[n / 2], v, acc);
-            }
+        for (int n = 0; n < E; n += 4) {
+            const float4 Bv = Bp[n / 4], Cv = Cp[n / 4];
+            float2 v = fma2(l2, make_float2(s[n], s[n + 1]), mul2(x2, make_float2(Bv.x, Bv.y)));
+            s[n] = v.x; s[n + 1] = v.y;
+            acc = fma2(make_float2(Cv.x, Cv.y), v, acc);
+            v = fma2(l2, make_float2(s[n + 2], s[n + 3]), mul2(x2, make_float2(Bv.z, Bv.w)));
+            s[n + 2] = v.x; s[n + 3] = v.y;
+            acc = fma2(make_float2(Cv.z, Cv.w), v, acc);
         }
         const float y = grp_sum<LPR>(__fadd_rn(acc.x, acc.y));
         if (p < pv.P && j == 0)
@@ -145,7 +128,7 @@ __device__ __forceinline__ void single_unit(const PoolView& pv, const RaggedCall
 
 template <int FMT, int N, int TYPE>
 __device__ __forceinline__ void single_tokens(const PoolView& pv, const RaggedCall& rc, int steps,
-                                              int blocks)
+                                              int blocks, float* sB, float* sC)
 {
     const int rows = steps * Shape<N>::RPW;
     const int tiles = (pv.P + rows - 1) / rows;
@@ -163,11 +146,11 @@ __device__ __forceinline__ void single_tokens(const PoolView& pv, const RaggedCa
         const int n = min(steps, (pv.P - p0 + Shape<N>::RPW - 1) / Shape<N>::RPW);
         if constexpr (Fmt<FMT>::quant) {
             if (!place.quant) {
-                single_unit<SSQ_F32, N, TYPE>(pv, rc, run, place, h, p0, n);
+                single_unit<SSQ_F32, N, TYPE>(pv, rc, run, place, h, p0, n, sB, sC);
                 continue;
             }
         }
-        single_unit<FMT, N, TYPE>(pv, rc, run, place, h, p0, n);
+        single_unit<FMT, N, TYPE>(pv, rc, run, place, h, p0, n, sB, sC);
     }
 }
 
@@ -205,21 +188,6 @@ __device__ __forceinline__ void write_plan(const PoolView& pv, const RaggedCall&
         rc.plan->next[0] = 0;
         rc.plan->next[1] = 0;
     }
-}
-
-// Where entry n of B or C is staged: lane by lane, in the order in which a
-// lane holds the entries of its row.
-template <int RF, int N>
-__device__ __forceinline__ int staged_row(int n)
-{
-    constexpr int E = Shape<N>::E, LPR = Shape<N>::LPR, PE = kPiece<RF, N>;
-    const int piece = n / PE;
-    return (piece % LPR) * (E + 4) + piece / LPR * PE + n % PE;
-}
-template <int FMT, int N>
-__device__ __forceinline__ int staged_at(bool quant, int n)
-{
-    return !Fmt<FMT>::quant || quant ? staged_row<FMT, N>(n) : staged_row<SSQ_F32, N>(n);
 }
 
 // A run of several tokens on `rows` rows of one head; the whole block.
@@ -304,7 +272,9 @@ tokens_kernel(const __grid_constant__ PoolView pv, const __grid_constant__ Ragge
     __shared__ int list[kThreads], count[kThreads / 32];
 
     if (rc.plan && blockIdx.x == 0) write_plan(pv, rc);
-    single_tokens<FMT, N, TYPE>(pv, rc, steps, gridDim.x);
+    static_assert(kTok >= kThreads / 32, "a staged row for every warp");
+    single_tokens<FMT, N, TYPE>(pv, rc, steps, gridDim.x, sB[threadIdx.x / 32],
+                                sC[threadIdx.x / 32]);
 
     const int tid = threadIdx.x;
     const int rows = blockDim.x / LPR;

@@ -28,7 +28,7 @@ struct RaggedCall {
     long long xs, Bs, Cs, dts, ys;   // token strides in elements
     // chunk kernel: segments of seg_chunks chunks; states [batch][nseg][H][P][N]
     // and decays [batch][nseg][H] of the workspace (nseg > 1)
-    int nseg, seg_chunks;
+    int nseg, seg_chunks, units_per_block;
     ChunkPlan* plan;                 // null: no run goes through chunks
     float* ws_state;
     float* ws_decay;
@@ -73,7 +73,11 @@ cudaError_t launch_ragged_tokens(const PoolView& pv, const RaggedCall& rc, int f
                                  cudaStream_t st);
 cudaError_t launch_ragged_chunks(const PoolView& pv, const RaggedCall& rc, int fmt,
                                  cudaStream_t st);
-// Segments that the longest run is cut into, and their length in chunks.
-void chunk_plan(int H, int P, int G, int batch, int max_len, int* nseg, int* seg_chunks);
+// Segments that the longest run is cut into, their length in chunks, and the
+// units (64 rows of a head) of a block.
+struct ChunkShape {
+    int nseg, seg_chunks, units_per_block;
+};
+void chunk_plan(int H, int P, int G, int batch, int max_len, ChunkShape* cs);
 
 }  // namespace ssq

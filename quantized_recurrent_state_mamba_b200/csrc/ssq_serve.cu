@@ -76,7 +76,7 @@ bool chunks_fit(const ssq_config* cfg, int max_len, const ssq_tokens* t)
 // longest is cut into nseg > 1 segments a state and a decay per request,
 // segment and head.  Offsets in bytes.
 struct Workspace {
-    int nseg, seg_chunks;
+    ssq::ChunkShape cs;
     size_t state, decay, total;
 };
 Workspace workspace_of(const ssq_config* cfg, int batch, int max_len)
@@ -84,12 +84,11 @@ Workspace workspace_of(const ssq_config* cfg, int batch, int max_len)
     Workspace w;
     memset(&w, 0, sizeof(w));
     if (batch < 1 || !chunks_shape(cfg, max_len)) return w;
-    ssq::chunk_plan(cfg->nheads, cfg->headdim, cfg->ngroups, batch, max_len, &w.nseg,
-                    &w.seg_chunks);
-    const size_t places = (size_t)batch * w.nseg;
+    ssq::chunk_plan(cfg->nheads, cfg->headdim, cfg->ngroups, batch, max_len, &w.cs);
+    const size_t places = (size_t)batch * w.cs.nseg;
     w.state = (sizeof(ssq::ChunkPlan) + places * sizeof(int2) + 255) / 256 * 256;
     w.decay = w.total = w.state;
-    if (w.nseg > 1) {
+    if (w.cs.nseg > 1) {
         w.decay += places * cfg->nheads * cfg->headdim * cfg->d_state * 4;
         w.total = w.decay + places * cfg->nheads * 4;
     }
@@ -188,8 +187,9 @@ ssq_status ssq_prefill_ragged(const ssq_config* cfg, void* pool, const int32_t* 
     if (chunked) {
         char* base = static_cast<char*>(workspace);
         rc.chunk_min = kChunkMin;
-        rc.nseg = ws.nseg;
-        rc.seg_chunks = ws.seg_chunks;
+        rc.nseg = ws.cs.nseg;
+        rc.seg_chunks = ws.cs.seg_chunks;
+        rc.units_per_block = ws.cs.units_per_block;
         rc.plan = reinterpret_cast<ssq::ChunkPlan*>(base);
         rc.ws_state = reinterpret_cast<float*>(base + ws.state);
         rc.ws_decay = reinterpret_cast<float*>(base + ws.decay);
