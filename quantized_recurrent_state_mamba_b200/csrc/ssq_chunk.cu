@@ -108,8 +108,11 @@ static_assert(kSmemBytes <= 227 * 1024, "shared memory");
 constexpr int kTmemCols = 512;
 constexpr uint32_t kColG = 0;
 __host__ __device__ constexpr uint32_t col_m(int u) { return 128 + 192 * u; }
-__host__ __device__ constexpr uint32_t col_y1(int u) { return col_m(u) + 64; }   // and dS
+__host__ __device__ constexpr uint32_t col_y1(int u) { return col_m(u) + 64; }
 __host__ __device__ constexpr uint32_t col_y2(int u) { return col_m(u) + 128; }
+// dS takes Y1's columns; in the first pass the units' lie side by side.
+template <bool STATE>
+__host__ __device__ constexpr uint32_t col_ds(int u) { return STATE ? 128 + 64 * u : col_y1(u); }
 
 __device__ __forceinline__ void unit_sync(int u)
 {
@@ -527,7 +530,7 @@ __device__ __forceinline__ bool unit_loop(const PoolView& pv, const RaggedCall& 
 #pragma unroll
             for (int k = 0; k < kPH; k += 16) {
                 float d[16];
-                tc::ld16(tm + col_y1(u) + kPH * hf + k, d);
+                tc::ld16(tm + col_ds<STATE>(u) + kPH * hf + k, d);
                 tc::wait_ld(d);
                 if (k + 16 == kPH) {
                     tc::fence_before();
@@ -675,19 +678,49 @@ __device__ __forceinline__ bool issue_g(unsigned base, Tail& tl, uint32_t tmem, 
     return true;
 }
 
+// First pass: dS of both units in one product (B is read once for the two;
+// the units' parts of w X are one operand of two 64-row pieces).
+template <int NU>
+__device__ __forceinline__ bool issue_state(unsigned base, Tail& tl, uint32_t tmem, int nc,
+                                            int parts)
+{
+    constexpr uint32_t kShape = tc::shape(128, 64 * NU, true, true);
+    using M = Mem<true>;
+    for (int c = 0; c < nc; ++c) {
+        const unsigned sb = base + slot_b<true>(c) * kTileCB;
+        bool ok = tc::wait_phase(&tl.cb_full[slot_b<true>(c)], phase_b<true>(c));
+        for (int u = 0; u < NU; ++u) ok = ok && tc::wait_phase(&tl.xs_ready[u], c & 1);
+        if (!__all_sync(0xffffffffu, ok)) return false;
+        if (tc::elect()) {
+            tc::fence_after();
+            const uint64_t db = tc::operand(sb, kTileX), dx = tc::operand(base + M::xs, M::xs_unit);
+#pragma unroll
+            for (int part = 0; part < 3; ++part)
+                if (part < parts)
+#pragma unroll
+                    for (int k = 0; k < kL / 16; ++k)
+                        tc::mma(tmem + col_ds<true>(0), db + k * 128,
+                                dx + (part * kTileX >> 4) + k * 128, kShape, part + k > 0);
+            for (int u = 0; u < NU; ++u) tc::commit(&tl.ds_full[u]);
+            tc::commit(&tl.cb_empty[slot_b<true>(c)]);
+        }
+        __syncwarp();
+    }
+    return true;
+}
+
 // dS, Y2 and Y1 of unit U.
-template <bool STATE, int U>
+template <int U>
 __device__ __forceinline__ bool issue_unit(unsigned base, Tail& tl, uint32_t tmem, int nc, int nu,
-                                           int last_len, int parts, int halves, int lane)
+                                           int last_len, int parts, int halves)
 {
     constexpr uint32_t kShapeY = tc::shape(128, 64, false, true);
     constexpr uint32_t kShapeS = tc::shape(128, 64, true, true);
-    using M = Mem<STATE>;
-    const unsigned xs = base + M::xs + U * M::xs_unit, so = base + M::s + U * kTileX;
+    using M = Mem<false>;
+    const unsigned xs = base + M::xs, so = base + M::s + U * kTileX;
     for (int c = 0; c < nc; ++c) {
-        const unsigned sb = base + slot_b<STATE>(c) * kTileCB;
-        bool ok = STATE ? tc::wait_phase(&tl.cb_full[slot_b<STATE>(c)], phase_b<STATE>(c))
-                        : tc::wait_phase(&tl.b_ready, c & 1);
+        const unsigned sb = base + slot_b<false>(c) * kTileCB;
+        bool ok = tc::wait_phase(&tl.b_ready, c & 1);
         ok = ok && tc::wait_phase(&tl.xs_ready[U], c & 1);
         if (!__all_sync(0xffffffffu, ok)) return false;
         // a partial chunk is always split in three
@@ -700,36 +733,32 @@ __device__ __forceinline__ bool issue_unit(unsigned base, Tail& tl, uint32_t tme
                 if (part < 2 || three)
 #pragma unroll
                     for (int k = 0; k < kL / 16; ++k)
-                        tc::mma(tmem + col_y1(U), db + k * 128, dx + (part * kTileX >> 4) + k * 128,
+                        tc::mma(tmem + col_ds<false>(U), db + k * 128, dx + (part * kTileX >> 4) + k * 128,
                                 kShapeS, part + k > 0);
             tc::commit(&tl.ds_full[U]);
-            tc::commit(&tl.cb_empty[slot_b<STATE>(c)]);
-            if constexpr (!STATE) {
-                const uint64_t dc = tc::operand(base + slot_c(c) * kTileCB), ds = tc::operand(so);
+            tc::commit(&tl.cb_empty[slot_b<false>(c)]);
+            const uint64_t dc = tc::operand(base + slot_c(c) * kTileCB), ds = tc::operand(so);
 #pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    if (k < 4 || halves == 2)
-                        tc::mma(tmem + col_y2(U), dc + (((k >> 2) * kTileX + (k & 3) * 32) >> 4),
-                                ds + k * 128, kShapeY, k > 0);
-                tc::commit(&tl.cb_empty[slot_c(c)]);
-            }
+            for (int k = 0; k < 8; ++k)
+                if (k < 4 || halves == 2)
+                    tc::mma(tmem + col_y2(U), dc + (((k >> 2) * kTileX + (k & 3) * 32) >> 4),
+                            ds + k * 128, kShapeY, k > 0);
+            tc::commit(&tl.cb_empty[slot_c(c)]);
         }
         __syncwarp();
-        if constexpr (!STATE) {
-            ok = tc::wait_phase(&tl.m_ready[U], c & 1);
-            if (!__all_sync(0xffffffffu, ok)) return false;
-            if (tc::elect()) {
-                tc::fence_after();
-                const uint64_t dx =
-                    tc::operand(base + M::x + ((c * nu + U) % M::ring_x) * kTileX);
+        ok = tc::wait_phase(&tl.m_ready[U], c & 1);
+        if (!__all_sync(0xffffffffu, ok)) return false;
+        if (tc::elect()) {
+            tc::fence_after();
+            const uint64_t dx =
+                tc::operand(base + M::x + ((c * nu + U) % M::ring_x) * kTileX);
 #pragma unroll
-                for (int k = 0; k < kL / 16; ++k)
-                    tc::mma_ta(tmem + col_y1(U), tmem + col_m(U) + k * 8, dx + k * 128, kShapeY,
-                               k > 0);
-                tc::commit(&tl.y_full[U]);
-            }
-            __syncwarp();
+            for (int k = 0; k < kL / 16; ++k)
+                tc::mma_ta(tmem + col_y1(U), tmem + col_m(U) + k * 8, dx + k * 128, kShapeY,
+                           k > 0);
+            tc::commit(&tl.y_full[U]);
         }
+        __syncwarp();
     }
     return true;
 }
@@ -805,7 +834,7 @@ chunk_kernel(const __grid_constant__ PoolView pv, const __grid_constant__ Ragged
             for (uint64_t* m = tl.cb_full; m < tl.drained + 3; ++m) mbar_inval(m);
         for (int i = 0; i < kMaxRing; ++i) {
             mbar_init(&tl.cb_full[i], 1);
-            mbar_init(&tl.cb_empty[i], STATE ? nu : nu + 1);
+            mbar_init(&tl.cb_empty[i], STATE ? 1 : nu + 1);
             mbar_init(&tl.x_full[i], 1);
             mbar_init(&tl.x_empty[i], 1);
         }
@@ -938,13 +967,16 @@ chunk_kernel(const __grid_constant__ PoolView pv, const __grid_constant__ Ragged
     } else {
         // ---- products ----
         const int last_len = wk.run.len - (wk.c0 + nc - 1) * kL;
-        if (warp == kElemWarps + 1) {
-            if constexpr (!STATE)
-                ok = issue_g(base, tl, tmem, nc, last_len, halves, lane);
+        if constexpr (STATE) {
+            if (warp == kElemWarps + 1)
+                ok = nu > 1 ? issue_state<2>(base, tl, tmem, nc, parts)
+                            : issue_state<1>(base, tl, tmem, nc, parts);
+        } else if (warp == kElemWarps + 1) {
+            ok = issue_g(base, tl, tmem, nc, last_len, halves, lane);
         } else if (warp == kElemWarps + 2) {
-            ok = issue_unit<STATE, 0>(base, tl, tmem, nc, nu, last_len, parts, halves, lane);
+            ok = issue_unit<0>(base, tl, tmem, nc, nu, last_len, parts, halves);
         } else if (nu > 1) {
-            ok = issue_unit<STATE, 1>(base, tl, tmem, nc, nu, last_len, parts, halves, lane);
+            ok = issue_unit<1>(base, tl, tmem, nc, nu, last_len, parts, halves);
         }
         // the products are complete before the memory they use goes away
         if (tc::elect()) {
