@@ -134,7 +134,7 @@ __device__ __forceinline__ void single_tokens(const PoolView& pv, const RaggedCa
     const int tiles = (pv.P + rows - 1) / rows;
     const int per = tiles * pv.H;
     const long long units = (long long)per * rc.batch;
-    const int warps = blockDim.x / 32;
+    constexpr int warps = kThreads / 32;
     for (long long i = (long long)blockIdx.x * warps + threadIdx.x / 32; i < units;
          i += (long long)blocks * warps) {
         const int b = (int)(i / per), unit = (int)(i - (long long)b * per);
@@ -158,9 +158,9 @@ __device__ __forceinline__ void single_tokens(const PoolView& pv, const RaggedCa
 __device__ __forceinline__ void write_plan(const PoolView& pv, const RaggedCall& rc)
 {
     __shared__ int warp_sum[kThreads / 32];
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid / 32, warps = blockDim.x / 32;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid / 32, warps = kThreads / 32;
     int base = 0;
-    for (int b0 = 0; b0 < rc.batch; b0 += blockDim.x) {
+    for (int b0 = 0; b0 < rc.batch; b0 += kThreads) {
         const int b = b0 + tid;
         int n = 0;
         if (b < rc.batch) {
@@ -211,26 +211,48 @@ __device__ __forceinline__ void run_unit(const PoolView& pv, const RaggedCall& r
     } else {
         row_load<FMT, N>(place, p, j, active, s);
     }
+    // A thread's share of the staged B and C, one x per token, and (the first
+    // threads) a dt: loaded for the next tokens while these are worked on.
+    constexpr int kShare = kTok * N > kThreads ? kTok * N / kThreads : 1;
+    float nB[kShare], nC[kShare], nx[kTok], ndt = 0.0f;
+    auto fetch = [&](int c0) {
+        const long long t0 = (long long)run.t0 + c0;
+        const int nt = min(kTok, run.len - c0);
+#pragma unroll
+        for (int k = 0; k < kShare; ++k) {
+            const int i = tid + k * kThreads, t = i / N, n = i % N;
+            const bool in = t < nt;
+            nB[k] = in ? load_act<TYPE>(rc.B, (t0 + t) * rc.Bs + (long long)g * N + n) : 0.0f;
+            nC[k] = in ? load_act<TYPE>(rc.C, (t0 + t) * rc.Cs + (long long)g * N + n) : 0.0f;
+        }
+        ndt = tid < nt ? __ldg(rc.dt + (t0 + tid) * rc.dts + h) : 0.0f;
+#pragma unroll
+        for (int t = 0; t < kTok; ++t)
+            nx[t] = active && t < nt ? load_act<TYPE>(rc.x, (t0 + t) * rc.xs + at) : 0.0f;
+    };
+    if (run.len > 0) fetch(0);
     for (int c0 = 0; c0 < run.len; c0 += kTok) {
         const int nt = min(kTok, run.len - c0);
         const long long t0 = (long long)run.t0 + c0;
         __syncthreads();
-        for (int i = tid; i < nt * N; i += blockDim.x) {
-            const int t = i / N, n = i % N;
-            const int to = staged_at<FMT, N>(place.quant, n);
-            sB[t][to] = load_act<TYPE>(rc.B, (t0 + t) * rc.Bs + (long long)g * N + n);
-            sC[t][to] = load_act<TYPE>(rc.C, (t0 + t) * rc.Cs + (long long)g * N + n);
+#pragma unroll
+        for (int k = 0; k < kShare; ++k) {
+            const int i = tid + k * kThreads, t = i / N, n = i % N;
+            if (t < nt) {
+                const int to = staged_at<FMT, N>(place.quant, n);
+                sB[t][to] = nB[k];
+                sC[t][to] = nC[k];
+            }
         }
         if (tid < nt) {
-            const float dt = __ldg(rc.dt + (t0 + tid) * rc.dts + h);
-            sDt[tid] = dt;
-            sLam[tid] = decay(dt, A);
+            sDt[tid] = ndt;
+            sLam[tid] = decay(ndt, A);
         }
         float xs[kTok];
 #pragma unroll
-        for (int t = 0; t < kTok; ++t)
-            xs[t] = active && t < nt ? load_act<TYPE>(rc.x, (t0 + t) * rc.xs + at) : 0.0f;
+        for (int t = 0; t < kTok; ++t) xs[t] = nx[t];
         __syncthreads();
+        if (c0 + kTok < run.len) fetch(c0 + kTok);
 #pragma unroll
         for (int t = 0; t < kTok; ++t) {
             if (t >= nt) break;
@@ -276,12 +298,12 @@ tokens_kernel(const __grid_constant__ PoolView pv, const __grid_constant__ Ragge
     single_tokens<FMT, N, TYPE>(pv, rc, steps, gridDim.x, sB[threadIdx.x / 32],
                                 sC[threadIdx.x / 32]);
 
+    constexpr int rows = kThreads / LPR;
     const int tid = threadIdx.x;
-    const int rows = blockDim.x / LPR;
     const int tiles = (pv.P + rows - 1) / rows, per = tiles * pv.H;
     int skip = blockIdx.x;                           // units until this block's next one
-    for (int b0 = 0; b0 < rc.batch; b0 += blockDim.x) {
-        // the runs among the next blockDim.x requests
+    for (int b0 = 0; b0 < rc.batch; b0 += kThreads) {
+        // the runs among the next requests
         __syncthreads();
         bool take = false;
         if (b0 + tid < rc.batch) {
@@ -292,7 +314,7 @@ tokens_kernel(const __grid_constant__ PoolView pv, const __grid_constant__ Ragge
         if (tid % 32 == 0) count[tid / 32] = __popc(mine);
         if (!__syncthreads_or(take)) continue;
         int found = 0, before = 0;
-        for (int w = 0; w < (int)blockDim.x / 32; ++w) {
+        for (int w = 0; w < kThreads / 32; ++w) {
             if (w < tid / 32) before += count[w];
             found += count[w];
         }
@@ -313,11 +335,8 @@ template <int FMT, int N>
 cudaError_t launch_n(const PoolView& pv, const RaggedCall& rc, cudaStream_t st)
 {
     constexpr int LPR = Shape<N>::LPR;
-    // Blocks of whole warps over a head's rows, on a grid that is resident at
-    // once (two blocks per SM).
-    int threads = (pv.P * LPR + 31) / 32 * 32;
-    if (threads > kThreads) threads = kThreads;
-    const int rows = threads / LPR, warps = threads / 32;
+    // A grid that is resident at once (two blocks per SM).
+    constexpr int warps = kThreads / 32, rows = kThreads / LPR;
     const long long resident = 2LL * kSMs;
     // Single tokens: a warp takes up to 8 groups of rows of a head, fewer where
     // that would leave warps without work.
@@ -335,9 +354,9 @@ cudaError_t launch_n(const PoolView& pv, const RaggedCall& rc, cudaStream_t st)
     }
     const unsigned grid = (unsigned)(blocks < resident ? blocks : resident);
     switch (rc.type) {
-    case SSQ_T_BF16: tokens_kernel<FMT, N, SSQ_T_BF16><<<grid, threads, 0, st>>>(pv, rc, steps); break;
-    case SSQ_T_F16: tokens_kernel<FMT, N, SSQ_T_F16><<<grid, threads, 0, st>>>(pv, rc, steps); break;
-    default: tokens_kernel<FMT, N, SSQ_T_F32><<<grid, threads, 0, st>>>(pv, rc, steps); break;
+    case SSQ_T_BF16: tokens_kernel<FMT, N, SSQ_T_BF16><<<grid, kThreads, 0, st>>>(pv, rc, steps); break;
+    case SSQ_T_F16: tokens_kernel<FMT, N, SSQ_T_F16><<<grid, kThreads, 0, st>>>(pv, rc, steps); break;
+    default: tokens_kernel<FMT, N, SSQ_T_F32><<<grid, kThreads, 0, st>>>(pv, rc, steps); break;
     }
     return cudaGetLastError();
 }
