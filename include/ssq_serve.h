@@ -62,8 +62,8 @@ typedef struct {
 } ssq_tokens;
 
 /* Bytes of device workspace that ssq_prefill_ragged takes for a batch of
- * this size whose longest run has max_len tokens (0: none needed).  Host
- * only; no CUDA call. */
+ * this size and this max_len, for activations of any type (0: none needed).
+ * Host only; no CUDA call. */
 SSQ_API ssq_status ssq_prefill_ragged_workspace(const ssq_config* cfg, int batch, int max_len,
                                                 size_t* bytes);
 
@@ -80,16 +80,19 @@ SSQ_API ssq_status ssq_prefill_ragged_workspace(const ssq_config* cfg, int batch
  * unless it is fresh (then the zero state is written).
  *
  * Runs of at least 32 tokens in bf16 (headdim a multiple of 8, d_state at most 128,
- * strides and pointers of x, B, C multiples of 16 bytes) go through chunks of
- * 128 tokens on the tensor cores: within a chunk, with cs the running sum of
+ * strides and pointers of x, B, C and y multiples of 16 bytes) go through chunks
+ * of 128 tokens on the tensor cores: within a chunk, with cs the running sum of
  * a,
  *     y_i = sum_{j<=i} (C_i.B_j) exp(cs_i-cs_j) dt_j x_j + exp(cs_i) S C_i
  *     S   = exp(cs_L) S + sum_j exp(cs_L-cs_j) dt_j x_j B_j^T
  * with fp32 sums and state; the products' operands are bf16, the last one's
- * input taken as a sum of two bf16 parts.  Other runs go token by token in
- * fp32 arithmetic.  Either way a non-finite x, B, C or dt acts on its own and
- * later tokens of its own request only; in a chunk a non-finite x_p makes y
- * and the state of its row p NaN.
+ * input taken as a sum of bf16 parts: two, or three for rows stored in fp32.
+ * Other runs go token by token in fp32 arithmetic, the operations and their
+ * order those of ssq_prefill.  Either way a long run on few heads may be cut
+ * into segments whose states are joined in fp32, by a rule on the shape, batch
+ * and max_len.  A non-finite x, B, C or dt acts on its own and later tokens of
+ * its own request only; in a chunk a non-finite x_p makes y and the state of
+ * its row p NaN.
  *
  *   slot_idx   device int32 [batch] or NULL (slot b)
  *   cu_tokens  device int32 [batch+1], not decreasing, within [0, total]; a

@@ -32,7 +32,7 @@
 // the state's row p NaN.
 //
 // Long runs on few heads are cut into segments: a first pass computes each
-// segment's own state and decay, ssq_chunk_join turns them into the states
+// segment's own state and decay, segment_join turns them into the states
 // the segments start from, and the main pass runs all segments at once.
 #include <cstring>
 
@@ -813,8 +813,9 @@ chunk_kernel(const __grid_constant__ PoolView pv, const __grid_constant__ Ragged
         wk.run = ragged_run(pv, rc, wk.b, false);   // (the token kernel reports)
         const int chunks = (wk.run.len + kL - 1) / kL;
         wk.nseg = run_segments(rc, wk.run.len);
-        wk.c0 = wk.seg * rc.seg_chunks;
-        wk.nc = min(rc.seg_chunks, chunks - wk.c0);
+        const int seg_chunks = rc.nseg > 1 ? rc.seg_tokens / kL : chunks;
+        wk.c0 = wk.seg * seg_chunks;
+        wk.nc = min(seg_chunks, chunks - wk.c0);
     }
     __syncthreads();
     const int nu = wk.nu, nc = wk.nc;
@@ -1005,7 +1006,7 @@ constexpr int kJoinThreads = 128;
 
 template <int FMT, int N>
 __global__ void __launch_bounds__(kJoinThreads)
-chunk_join(const __grid_constant__ PoolView pv, const __grid_constant__ RaggedCall rc)
+segment_join(const __grid_constant__ PoolView pv, const __grid_constant__ RaggedCall rc)
 {
     constexpr int E = Shape<N>::E, LPR = Shape<N>::LPR;
     constexpr int kRows = kJoinThreads / LPR;        // kRows*N = 128*E floats
@@ -1016,7 +1017,7 @@ chunk_join(const __grid_constant__ PoolView pv, const __grid_constant__ RaggedCa
     const int b = blockIdx.x / per, unit = blockIdx.x - b * per;
     const int pos = unit / tiles, h = pv.perm[pos], r0 = unit % tiles * kRows;
     const Run run = ragged_run(pv, rc, b, false);
-    if (!run.ok || run.len < rc.chunk_min) return;
+    if (!run.ok || (rc.plan && run.len < rc.chunk_min)) return;
     const int nseg = run_segments(rc, run.len);
     if (nseg < 2) return;
     const int tid = threadIdx.x, j = tid % LPR, r = tid / LPR;
@@ -1071,7 +1072,7 @@ cudaError_t join_n(const PoolView& pv, const RaggedCall& rc, cudaStream_t st)
     constexpr int kRows = kJoinThreads / Shape<N>::LPR;
     const long long grid = (long long)((pv.P + kRows - 1) / kRows) * pv.H * rc.batch;
     if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-    chunk_join<FMT, N><<<(unsigned)grid, kJoinThreads, 0, st>>>(pv, rc);
+    segment_join<FMT, N><<<(unsigned)grid, kJoinThreads, 0, st>>>(pv, rc);
     return cudaGetLastError();
 }
 template <int FMT>
@@ -1081,7 +1082,8 @@ cudaError_t join_fmt(const PoolView& pv, const RaggedCall& rc, cudaStream_t st)
     case 16: return join_n<FMT, 16>(pv, rc, st);
     case 32: return join_n<FMT, 32>(pv, rc, st);
     case 64: return join_n<FMT, 64>(pv, rc, st);
-    default: return join_n<FMT, 128>(pv, rc, st);
+    case 128: return join_n<FMT, 128>(pv, rc, st);
+    default: return join_n<FMT, 256>(pv, rc, st);
     }
 }
 cudaError_t join(const PoolView& pv, const RaggedCall& rc, int fmt, cudaStream_t st)
@@ -1150,28 +1152,30 @@ cudaError_t launch_pass(const PoolView& pv, const RaggedCall& rc, const ChunkMap
 
 }  // namespace
 
-void chunk_plan(int H, int P, int G, int batch, int max_len, ChunkShape* cs)
+RaggedPlan chunk_plan(int H, int P, int G, int batch, int max_len)
 {
-    cs->nseg = 1;
-    cs->seg_chunks = 0x7fffffff / kL;               // a run is one segment
-    cs->units_per_block = 2;
-    if (batch < 1) return;
+    RaggedPlan p = {1, 0, 2};
+    if (batch < 1) return p;
     // A block with one unit takes 6000 cycles a chunk, with two 7700: one each
     // where every unit gets an SM of its own.
     const int chunks = (int)(((long long)max_len + kL - 1) / kL);
-    if (chunk_items(H, P, G, 1) * batch <= kSMs) cs->units_per_block = 1;
-    // Segments of four chunks or more, while they fit the SMs at once: the
-    // first pass costs about half a main pass again.
-    const long long fit = kSMs / (chunk_items(H, P, G, cs->units_per_block) * batch);
-    const long long n = chunks / 4 < fit ? chunks / 4 : fit;
-    if (n < 2) return;
-    // with segments every SM is busy: two units a block
-    const long long fit2 = kSMs / (chunk_items(H, P, G, 2) * batch);
-    const long long n2 = chunks / 4 < fit2 ? chunks / 4 : fit2;
-    if (n2 > n) cs->units_per_block = 2;
-    const long long m = n2 > n ? n2 : n;
-    cs->seg_chunks = (int)((chunks + m - 1) / m);
-    cs->nseg = (chunks + cs->seg_chunks - 1) / cs->seg_chunks;
+    const long long one = chunk_items(H, P, G, 1) * batch, two = chunk_items(H, P, G, 2) * batch;
+    if (one <= kSMs) p.units_per_block = 1;
+    // Segments of four chunks or more, while all fit the SMs at once (two
+    // units a block); the first pass costs about half a main pass again.
+    const long long fit = kSMs / two, n = chunks / 4 < fit ? chunks / 4 : fit;
+    if (n < 2) return p;
+    const int seg_chunks = (int)((chunks + n - 1) / n);
+    p.seg_tokens = seg_chunks * kL;
+    p.nseg = (chunks + seg_chunks - 1) / seg_chunks;
+    if (one * p.nseg > kSMs) p.units_per_block = 2;
+    return p;
+}
+
+cudaError_t launch_segment_join(const PoolView& pv, const RaggedCall& rc, int fmt,
+                                cudaStream_t st)
+{
+    return join(pv, rc, fmt, st);
 }
 
 cudaError_t launch_ragged_chunks(const PoolView& pv, const RaggedCall& rc, int fmt,

@@ -7,10 +7,15 @@
 // registers for the whole run.  A block owns up to 256/LPR rows of one head of
 // one request (LPR = d_state/32 lanes per row), so B, C, dt and exp(dt*A) are
 // uniform in the block: they are converted to fp32 in shared memory once per
-// kTok tokens.  The pieces of B and C that a row's lanes read lie 36 floats
-// apart, so that the lanes' 16-byte reads hit different banks.  For a single
-// token the kernel is bound by the pool's traffic; for long runs by the fp32
-// pipe and the chain from token to token.
+// kTok tokens, the next tokens' loaded meanwhile (65536 fp16 tokens of 24 heads:
+// 71 ms without, 47 ms with).  The pieces of B and C that a row's lanes read lie
+// 36 floats apart, so that the lanes' 16-byte reads hit different banks.
+//
+// Bound: a single token by the pool's traffic (256 requests of 24 x 64 x 128 in
+// int8: 73 us, floor 61.6); long runs by the fp32 pipe and the chain from token
+// to token (14 operations a row entry and token; 8 x 2048 fp32 tokens of 32
+// heads: 1.43 ms).  Long runs on few heads are cut into segments, whose states
+// segment_join (ssq_chunk.cu) turns into those they start from.
 #include <cuda_fp16.h>
 
 #include "ssq_ragged.h"
@@ -190,11 +195,20 @@ __device__ __forceinline__ void write_plan(const PoolView& pv, const RaggedCall&
     }
 }
 
-// A run of several tokens on `rows` rows of one head; the whole block.
+// Which part of a run run_unit takes, where its state comes from and goes to.
+struct Part {
+    int t0, len;         // tokens
+    float* state;        // the segment's in the workspace; null: the run is whole
+    float* decay;        // state pass: from zero, no y, to the workspace
+    bool last;           // the state goes to the pool
+};
+
+// Tokens of a run on the rows of one head that the block covers.
 template <int FMT, int N, int TYPE>
 __device__ __forceinline__ void run_unit(const PoolView& pv, const RaggedCall& rc, const Run& run,
-                                         int pos, int p, float (&sB)[kTok][kRowF<N>],
-                                         float (&sC)[kTok][kRowF<N>], float* sLam, float* sDt)
+                                         const Part& part, int pos, int p,
+                                         float (&sB)[kTok][kRowF<N>], float (&sC)[kTok][kRowF<N>],
+                                         float* sLam, float* sDt)
 {
     constexpr int E = Shape<N>::E, LPR = Shape<N>::LPR;
     const int tid = threadIdx.x, j = tid % LPR;
@@ -204,8 +218,14 @@ __device__ __forceinline__ void run_unit(const PoolView& pv, const RaggedCall& r
     const RowPlace place = place_head<FMT>(pv, run.slot, rc.layer, pos);
     const long long at = (long long)h * pv.P + p;
 
-    float s[E];
-    if (run.fresh) {
+    // the thread's row in the workspace
+    float* seg = part.state ? part.state + ((long long)h * pv.P + p) * N : nullptr;
+    float s[E], all = 1.0f;
+    if (seg && !part.decay) {
+#pragma unroll
+        for (int n = 0; n < E; ++n) s[n] = 0.0f;
+        if (active) row_from_stage<FMT, N>(place, s, j, seg);
+    } else if (run.fresh || part.decay) {
 #pragma unroll
         for (int n = 0; n < E; ++n) s[n] = 0.0f;
     } else {
@@ -216,8 +236,8 @@ __device__ __forceinline__ void run_unit(const PoolView& pv, const RaggedCall& r
     constexpr int kShare = kTok * N > kThreads ? kTok * N / kThreads : 1;
     float nB[kShare], nC[kShare], nx[kTok], ndt = 0.0f;
     auto fetch = [&](int c0) {
-        const long long t0 = (long long)run.t0 + c0;
-        const int nt = min(kTok, run.len - c0);
+        const long long t0 = (long long)part.t0 + c0;
+        const int nt = min(kTok, part.len - c0);
 #pragma unroll
         for (int k = 0; k < kShare; ++k) {
             const int i = tid + k * kThreads, t = i / N, n = i % N;
@@ -230,10 +250,10 @@ __device__ __forceinline__ void run_unit(const PoolView& pv, const RaggedCall& r
         for (int t = 0; t < kTok; ++t)
             nx[t] = active && t < nt ? load_act<TYPE>(rc.x, (t0 + t) * rc.xs + at) : 0.0f;
     };
-    if (run.len > 0) fetch(0);
-    for (int c0 = 0; c0 < run.len; c0 += kTok) {
-        const int nt = min(kTok, run.len - c0);
-        const long long t0 = (long long)run.t0 + c0;
+    if (part.len > 0) fetch(0);
+    for (int c0 = 0; c0 < part.len; c0 += kTok) {
+        const int nt = min(kTok, part.len - c0);
+        const long long t0 = (long long)part.t0 + c0;
         __syncthreads();
 #pragma unroll
         for (int k = 0; k < kShare; ++k) {
@@ -252,13 +272,14 @@ __device__ __forceinline__ void run_unit(const PoolView& pv, const RaggedCall& r
 #pragma unroll
         for (int t = 0; t < kTok; ++t) xs[t] = nx[t];
         __syncthreads();
-        if (c0 + kTok < run.len) fetch(c0 + kTok);
+        if (c0 + kTok < part.len) fetch(c0 + kTok);
 #pragma unroll
         for (int t = 0; t < kTok; ++t) {
             if (t >= nt) break;
             const float x = xs[t];
             const float dtx = __fmul_rn(sDt[t], x);
             const float lam = sLam[t];
+            all = __fmul_rn(all, lam);
             const float4* Bp = reinterpret_cast<const float4*>(&sB[t][j * (E + 4)]);
             const float4* Cp = reinterpret_cast<const float4*>(&sC[t][j * (E + 4)]);
             const float2 l2 = make_float2(lam, lam), x2 = make_float2(dtx, dtx);
@@ -274,11 +295,16 @@ __device__ __forceinline__ void run_unit(const PoolView& pv, const RaggedCall& r
                 acc = fma2(make_float2(Cv.z, Cv.w), v, acc);
             }
             const float y = grp_sum<LPR>(__fadd_rn(acc.x, acc.y));
-            if (active && j == 0)
+            if (active && j == 0 && !part.decay)
                 store_act<TYPE>(rc.y, (t0 + t) * rc.ys + at, __fmaf_rn(D, x, y));
         }
     }
-    row_store<FMT, N>(place, p, j, active, s, reinterpret_cast<uint32_t*>(pv.pool));
+    if (part.decay) {
+        if (active) row_to_stage<FMT, N>(place, s, j, seg);
+        if (p == 0 && j == 0) part.decay[h] = all;
+    } else if (part.last) {
+        row_store<FMT, N>(place, p, j, active, s, reinterpret_cast<uint32_t*>(pv.pool));
+    }
 }
 
 // Every block takes its share of the single tokens, then of the other runs
@@ -286,7 +312,7 @@ __device__ __forceinline__ void run_unit(const PoolView& pv, const RaggedCall& r
 template <int FMT, int N, int TYPE>
 __global__ void __launch_bounds__(kThreads, 2)
 tokens_kernel(const __grid_constant__ PoolView pv, const __grid_constant__ RaggedCall rc,
-              int steps)
+              int steps, bool state_pass)
 {
     constexpr int LPR = Shape<N>::LPR;
     __shared__ __align__(16) float sB[kTok][kRowF<N>], sC[kTok][kRowF<N>];
@@ -295,8 +321,9 @@ tokens_kernel(const __grid_constant__ PoolView pv, const __grid_constant__ Ragge
 
     if (rc.plan && blockIdx.x == 0) write_plan(pv, rc);
     static_assert(kTok >= kThreads / 32, "a staged row for every warp");
-    single_tokens<FMT, N, TYPE>(pv, rc, steps, gridDim.x, sB[threadIdx.x / 32],
-                                sC[threadIdx.x / 32]);
+    if (!state_pass)
+        single_tokens<FMT, N, TYPE>(pv, rc, steps, gridDim.x, sB[threadIdx.x / 32],
+                                    sC[threadIdx.x / 32]);
 
     constexpr int rows = kThreads / LPR;
     const int tid = threadIdx.x;
@@ -320,19 +347,34 @@ tokens_kernel(const __grid_constant__ PoolView pv, const __grid_constant__ Ragge
         }
         if (take) list[before + __popc(mine & ((1u << tid % 32) - 1))] = b0 + tid;
         __syncthreads();
-        const int units = found * per;
+        const int segs = rc.plan ? 1 : rc.nseg;      // (plan: chunks have them)
+        const int units = found * per * segs;
         for (; skip < units; skip += gridDim.x) {
-            const int b = list[skip / per], unit = skip % per;
+            const int entry = skip / per, unit = skip - entry * per;
+            const int b = list[entry / segs], seg = entry % segs;
             const Run run = ragged_run(pv, rc, b, false);
-            run_unit<FMT, N, TYPE>(pv, rc, run, unit / tiles, unit % tiles * rows + tid / LPR, sB,
-                                   sC, sLam, sDt);
+            const int n = segs > 1 ? run_segments(rc, run.len) : 1;
+            Part part = {run.t0, run.len, nullptr, nullptr, true};
+            if (n > 1) {
+                part.t0 += seg * rc.seg_tokens;
+                part.len = min(rc.seg_tokens, run.len - seg * rc.seg_tokens);
+                part.last = seg + 1 == n;
+                const long long at = (long long)b * rc.nseg + seg;
+                part.state = rc.ws_state + at * pv.H * pv.P * N;
+                if (state_pass) part.decay = rc.ws_decay + at * pv.H;
+            }
+            if (seg > 0 && seg >= n) continue;       // a run of no token has its one
+            if (state_pass && part.last) continue;   // its state is not needed
+            run_unit<FMT, N, TYPE>(pv, rc, run, part, unit / tiles,
+                                   unit % tiles * rows + tid / LPR, sB, sC, sLam, sDt);
         }
         skip -= units;
     }
 }
 
 template <int FMT, int N>
-cudaError_t launch_n(const PoolView& pv, const RaggedCall& rc, cudaStream_t st)
+cudaError_t launch_n(const PoolView& pv, const RaggedCall& rc, bool state_pass,
+                     cudaStream_t st)
 {
     constexpr int LPR = Shape<N>::LPR;
     // A grid that is resident at once (two blocks per SM).
@@ -348,46 +390,76 @@ cudaError_t launch_n(const PoolView& pv, const RaggedCall& rc, cudaStream_t st)
     const long long units = (long long)((pv.P + rows1 - 1) / rows1) * pv.H * rc.batch;
     long long blocks = (units + warps - 1) / warps;
     if (rc.max_len != 1) {
-        const long long runs = (long long)((pv.P + rows - 1) / rows) * pv.H * rc.batch;
+        const long long runs = (long long)((pv.P + rows - 1) / rows) * pv.H * rc.batch
+                               * (rc.plan ? 1 : rc.nseg);
         if (runs > 0x3fffffffLL) return cudaErrorInvalidConfiguration;
         if (blocks < runs) blocks = runs;
     }
     const unsigned grid = (unsigned)(blocks < resident ? blocks : resident);
     switch (rc.type) {
-    case SSQ_T_BF16: tokens_kernel<FMT, N, SSQ_T_BF16><<<grid, kThreads, 0, st>>>(pv, rc, steps); break;
-    case SSQ_T_F16: tokens_kernel<FMT, N, SSQ_T_F16><<<grid, kThreads, 0, st>>>(pv, rc, steps); break;
-    default: tokens_kernel<FMT, N, SSQ_T_F32><<<grid, kThreads, 0, st>>>(pv, rc, steps); break;
+    case SSQ_T_BF16: tokens_kernel<FMT, N, SSQ_T_BF16><<<grid, kThreads, 0, st>>>(pv, rc, steps, state_pass); break;
+    case SSQ_T_F16: tokens_kernel<FMT, N, SSQ_T_F16><<<grid, kThreads, 0, st>>>(pv, rc, steps, state_pass); break;
+    default: tokens_kernel<FMT, N, SSQ_T_F32><<<grid, kThreads, 0, st>>>(pv, rc, steps, state_pass); break;
     }
     return cudaGetLastError();
 }
 
 template <int FMT>
-cudaError_t launch_fmt(const PoolView& pv, const RaggedCall& rc, cudaStream_t st)
+cudaError_t launch_fmt(const PoolView& pv, const RaggedCall& rc, bool state_pass,
+                       cudaStream_t st)
 {
     switch (pv.N) {
-    case 16: return launch_n<FMT, 16>(pv, rc, st);
-    case 32: return launch_n<FMT, 32>(pv, rc, st);
-    case 64: return launch_n<FMT, 64>(pv, rc, st);
-    case 128: return launch_n<FMT, 128>(pv, rc, st);
-    case 256: return launch_n<FMT, 256>(pv, rc, st);
+    case 16: return launch_n<FMT, 16>(pv, rc, state_pass, st);
+    case 32: return launch_n<FMT, 32>(pv, rc, state_pass, st);
+    case 64: return launch_n<FMT, 64>(pv, rc, state_pass, st);
+    case 128: return launch_n<FMT, 128>(pv, rc, state_pass, st);
+    case 256: return launch_n<FMT, 256>(pv, rc, state_pass, st);
+    default: return cudaErrorInvalidValue;
+    }
+}
+
+cudaError_t launch_pass(const PoolView& pv, const RaggedCall& rc, int fmt, bool state_pass,
+                        cudaStream_t st)
+{
+    switch (fmt) {
+    case SSQ_F32: return launch_fmt<SSQ_F32>(pv, rc, state_pass, st);
+    case SSQ_BF16: return launch_fmt<SSQ_BF16>(pv, rc, state_pass, st);
+    case SSQ_I8_SYM: return launch_fmt<SSQ_I8_SYM>(pv, rc, state_pass, st);
+    case SSQ_I8_ASYM: return launch_fmt<SSQ_I8_ASYM>(pv, rc, state_pass, st);
+    case SSQ_I4_SYM: return launch_fmt<SSQ_I4_SYM>(pv, rc, state_pass, st);
+    case SSQ_I4_ASYM: return launch_fmt<SSQ_I4_ASYM>(pv, rc, state_pass, st);
     default: return cudaErrorInvalidValue;
     }
 }
 
 }  // namespace
 
+RaggedPlan token_plan(int H, int P, int N, int batch, int max_len)
+{
+    RaggedPlan p = {1, 0, 0};
+    if (batch < 1) return p;
+    // Segments of 256 tokens or more, while the blocks are resident at once
+    // (one run of 65536 tokens of 24 heads in fp16: 47 ms in one piece, 9.1 ms
+    // in twelve, although every token but the last segment's is taken twice).
+    const int rows = kThreads / (N > 32 ? N / 32 : 1);
+    const long long blocks = (long long)((P + rows - 1) / rows) * H * batch;
+    const long long fit = 2LL * kSMs / blocks, most = max_len / 256;
+    const long long n = most < fit ? most : fit;
+    if (n < 3) return p;
+    p.seg_tokens = (int)((max_len + n - 1) / n);
+    p.nseg = (max_len + p.seg_tokens - 1) / p.seg_tokens;
+    return p;
+}
+
 cudaError_t launch_ragged_tokens(const PoolView& pv, const RaggedCall& rc, int fmt,
                                  cudaStream_t st)
 {
-    switch (fmt) {
-    case SSQ_F32: return launch_fmt<SSQ_F32>(pv, rc, st);
-    case SSQ_BF16: return launch_fmt<SSQ_BF16>(pv, rc, st);
-    case SSQ_I8_SYM: return launch_fmt<SSQ_I8_SYM>(pv, rc, st);
-    case SSQ_I8_ASYM: return launch_fmt<SSQ_I8_ASYM>(pv, rc, st);
-    case SSQ_I4_SYM: return launch_fmt<SSQ_I4_SYM>(pv, rc, st);
-    case SSQ_I4_ASYM: return launch_fmt<SSQ_I4_ASYM>(pv, rc, st);
-    default: return cudaErrorInvalidValue;
+    if (!rc.plan && rc.nseg > 1) {
+        cudaError_t e = launch_pass(pv, rc, fmt, true, st);
+        if (e == cudaSuccess) e = launch_segment_join(pv, rc, fmt, st);
+        if (e != cudaSuccess) return e;
     }
+    return launch_pass(pv, rc, fmt, false, st);
 }
 
 }  // namespace ssq

@@ -26,9 +26,11 @@ struct RaggedCall {
     const float *dt, *A, *D;
     void* y;
     long long xs, Bs, Cs, dts, ys;   // token strides in elements
-    // chunk kernel: segments of seg_chunks chunks; states [batch][nseg][H][P][N]
-    // and decays [batch][nseg][H] of the workspace (nseg > 1)
-    int nseg, seg_chunks, units_per_block;
+    // Long runs are cut into up to nseg segments of seg_tokens tokens (those
+    // that go through chunks; in calls without chunks, all): states
+    // [batch][nseg][H][P][N] and decays [batch][nseg][H] of the workspace
+    int nseg, seg_tokens;
+    int units_per_block;       // of the chunk kernel
     ChunkPlan* plan;                 // null: no run goes through chunks
     float* ws_state;
     float* ws_decay;
@@ -60,11 +62,10 @@ __device__ __forceinline__ Run ragged_run(const PoolView& pv, const RaggedCall& 
     return r;
 }
 
-// Segments of a run in chunks of 128 tokens.
+// Segments of a run.
 __device__ __forceinline__ int run_segments(const RaggedCall& rc, int len)
 {
-    const int chunks = (len + 127) / 128;
-    return rc.nseg > 1 ? (chunks + rc.seg_chunks - 1) / rc.seg_chunks : 1;
+    return rc.nseg > 1 ? (len + rc.seg_tokens - 1) / rc.seg_tokens : 1;
 }
 
 // Token by token (ssq_ragged.cu), and in chunks on the tensor cores
@@ -73,11 +74,15 @@ cudaError_t launch_ragged_tokens(const PoolView& pv, const RaggedCall& rc, int f
                                  cudaStream_t st);
 cudaError_t launch_ragged_chunks(const PoolView& pv, const RaggedCall& rc, int fmt,
                                  cudaStream_t st);
-// Segments that the longest run is cut into, their length in chunks, and the
+// Between the passes over segments: the states that they start from.
+cudaError_t launch_segment_join(const PoolView& pv, const RaggedCall& rc, int fmt,
+                                cudaStream_t st);
+// Segments that the longest run is cut into, their length, and (chunks) the
 // units (64 rows of a head) of a block.
-struct ChunkShape {
-    int nseg, seg_chunks, units_per_block;
+struct RaggedPlan {
+    int nseg, seg_tokens, units_per_block;
 };
-void chunk_plan(int H, int P, int G, int batch, int max_len, ChunkShape* cs);
+RaggedPlan chunk_plan(int H, int P, int G, int batch, int max_len);
+RaggedPlan token_plan(int H, int P, int N, int batch, int max_len);
 
 }  // namespace ssq

@@ -72,23 +72,23 @@ bool chunks_fit(const ssq_config* cfg, int max_len, const ssq_tokens* t)
            && aligned(t->C, 16) && aligned(t->y, 16);
 }
 
-// The workspace of runs that go through chunks: the work list, and where the
-// longest is cut into nseg > 1 segments a state and a decay per request,
-// segment and head.  Offsets in bytes.
+// The workspace: the chunk kernel's work list, and where the longest run is
+// cut into nseg > 1 segments a state and a decay per request, segment and head.
+// Offsets in bytes.
 struct Workspace {
-    ssq::ChunkShape cs;
+    ssq::RaggedPlan plan;
     size_t state, decay, total;
 };
-Workspace workspace_of(const ssq_config* cfg, int batch, int max_len)
+Workspace workspace_of(const ssq_config* cfg, int batch, int max_len, bool chunked)
 {
     Workspace w;
     memset(&w, 0, sizeof(w));
-    if (batch < 1 || !chunks_shape(cfg, max_len)) return w;
-    ssq::chunk_plan(cfg->nheads, cfg->headdim, cfg->ngroups, batch, max_len, &w.cs);
-    const size_t places = (size_t)batch * w.cs.nseg;
-    w.state = (sizeof(ssq::ChunkPlan) + places * sizeof(int2) + 255) / 256 * 256;
+    w.plan = chunked ? ssq::chunk_plan(cfg->nheads, cfg->headdim, cfg->ngroups, batch, max_len)
+                     : ssq::token_plan(cfg->nheads, cfg->headdim, cfg->d_state, batch, max_len);
+    const size_t places = (size_t)batch * w.plan.nseg;
+    if (chunked) w.state = (sizeof(ssq::ChunkPlan) + places * sizeof(int2) + 255) / 256 * 256;
     w.decay = w.total = w.state;
-    if (w.cs.nseg > 1) {
+    if (w.plan.nseg > 1) {
         w.decay += places * cfg->nheads * cfg->headdim * cfg->d_state * 4;
         w.total = w.decay + places * cfg->nheads * 4;
     }
@@ -115,7 +115,14 @@ ssq_status ssq_prefill_ragged_workspace(const ssq_config* cfg, int batch, int ma
     if (batch < 0) return fail(SSQ_ERR_INVALID_ARG, "batch %d < 0", batch);
     if (max_len < 0) return fail(SSQ_ERR_INVALID_ARG, "max_len %d < 0", max_len);
     if (!bytes) return fail(SSQ_ERR_INVALID_ARG, "bytes is NULL");
-    *bytes = workspace_of(cfg, batch, max_len).total;
+    *bytes = 0;
+    if (batch < 1) return SSQ_OK;
+    // for activations of any type
+    *bytes = workspace_of(cfg, batch, max_len, false).total;
+    if (chunks_shape(cfg, max_len)) {
+        const size_t n = workspace_of(cfg, batch, max_len, true).total;
+        if (n > *bytes) *bytes = n;
+    }
     return SSQ_OK;
 }
 
@@ -152,14 +159,15 @@ ssq_status ssq_prefill_ragged(const ssq_config* cfg, void* pool, const int32_t* 
     }
     SSQ_TRY(need(A, "A", 4));
     SSQ_TRY(need(D, "D", 4));
-    const Workspace ws = workspace_of(cfg, batch, max_len);
-    if (ws.total > 0) {
-        SSQ_TRY(need(workspace, "workspace", 256));
-        if (workspace_bytes < ws.total)
-            return fail(SSQ_ERR_INVALID_ARG, "workspace of %zu bytes, need %zu", workspace_bytes,
-                        ws.total);
-    }
     if (batch == 0) return SSQ_OK;
+    size_t want = 0;
+    SSQ_TRY(ssq_prefill_ragged_workspace(cfg, batch, max_len, &want));
+    if (want > 0) {
+        SSQ_TRY(need(workspace, "workspace", 256));
+        if (workspace_bytes < want)
+            return fail(SSQ_ERR_INVALID_ARG, "workspace of %zu bytes, need %zu", workspace_bytes,
+                        want);
+    }
     ssq::RaggedCall rc;
     memset(&rc, 0, sizeof(rc));
     rc.slot_idx = slot_idx;
@@ -184,13 +192,16 @@ ssq_status ssq_prefill_ragged(const ssq_config* cfg, void* pool, const int32_t* 
     rc.dts = tok->dt_stride;
     rc.ys = tok->y_stride;
     const bool chunked = chunks_fit(cfg, max_len, tok);
+    const Workspace ws = workspace_of(cfg, batch, max_len, chunked);
+    char* base = static_cast<char*>(workspace);
     if (chunked) {
-        char* base = static_cast<char*>(workspace);
         rc.chunk_min = kChunkMin;
-        rc.nseg = ws.cs.nseg;
-        rc.seg_chunks = ws.cs.seg_chunks;
-        rc.units_per_block = ws.cs.units_per_block;
         rc.plan = reinterpret_cast<ssq::ChunkPlan*>(base);
+    }
+    rc.nseg = ws.plan.nseg;
+    rc.seg_tokens = ws.plan.seg_tokens;
+    rc.units_per_block = ws.plan.units_per_block;
+    if (rc.nseg > 1) {
         rc.ws_state = reinterpret_cast<float*>(base + ws.state);
         rc.ws_decay = reinterpret_cast<float*>(base + ws.decay);
     }

@@ -226,6 +226,28 @@ def test_chunks_segments(fmt, fresh):
     assert ssq.ssq_pool_error(cfg, pool) == 0
 
 
+@pytest.mark.parametrize("fmt,dtype,N,mask", [("f32", torch.float16, 128, None),
+                                              ("bf16", torch.float32, 256, None),
+                                              ("i8a", torch.float16, 16, None),
+                                              ("i4s", torch.float32, 64, [1, 0]),
+                                              ("i8s", torch.float16, 128, [0, 1])])
+def test_token_segments(fmt, dtype, N, mask):
+    """Types without chunks: a long run cut into segments of tokens (two
+    passes), beside one that ends in the second segment, one of a segment, a
+    single token and none, from stored and from fresh states."""
+    ssq = require_gpu()
+    lens = [1200, 290, 256, 1, 0, 0]
+    fresh = torch.tensor([0, 1, 0, 0, 0, 1], dtype=torch.uint8, device="cuda")
+    i = inputs(lens, 2, 20, N, 1, dtype, 19)
+    cfg = ssq.Config(1, 8, 2, 20, N, 1, fmt, mask)
+    assert ssq.ssq_prefill_ragged_workspace(cfg, 6, 1200) >= 6 * 4 * 2 * 20 * N * 4
+    y, b, a, pool, cfg = run(ssq, i, lens, fmt, fresh=fresh, mask=mask)
+    check(i, lens, fmt, y, b, a, fresh=fresh, mask=mask)
+    assert ssq.ssq_pool_error(cfg, pool) == 0
+    again, _, a2, _, _ = run(ssq, i, lens, fmt, fresh=fresh, mask=mask)
+    assert torch.equal(y, again) and torch.equal(a, a2)
+
+
 # ---------------------------------------------------------------------------
 # What a call may not touch, and what must not spread
 # ---------------------------------------------------------------------------

@@ -56,9 +56,11 @@ def test_workspace_sizes(ssq):
     assert need(0, 1000) == 0 and need(4, 0) == 0 and need(4, 31) == 0
     assert need(4, 32) > 0                      # runs of 32 tokens may go through chunks
     assert need(4, 32) % 256 == 0
-    # shapes that do not go through chunks need none
-    assert need(4, 4096, config(ssq, headdim=12)) == 0
-    assert need(4, 4096, config(ssq, d_state=256)) == 0
+    # token by token: nothing, until a run is worth cutting into segments
+    for odd in (config(ssq, headdim=12), config(ssq, d_state=256)):
+        assert need(4, 600, odd) == 0
+        assert need(4, 4096, odd) % (4 * 4 * (odd.c.headdim * odd.c.d_state + 1) * 4) == 0
+        assert need(4, 4096, odd) > 0
     # a long run on few heads is cut into segments: a state per request,
     # segment and head
     states = need(1, 65536) - need(1, 129)
