@@ -586,14 +586,15 @@ cudaError_t launch_one(const BeamCall& bc, int cs, cudaStream_t st)
 cudaError_t launch_beam(const BeamCall& bc, cudaStream_t st)
 {
     // Blocks per request (a cluster): as many as keep the batch within two
-    // blocks per SM and leave every warp a vector; 16, which must find 16 SMs
-    // of one GPC at once, only for batches that fill few GPCs (1 x 4 beams of
-    // 32000 logits: @@ us with 16, @@ with 8; 16 x 5 of 50001: 47 with 16, 28
-    // with 8).
+    // blocks per SM and leave every warp a vector.  16, which must find 16 SMs
+    // of one GPC at once, only for batches that fill few GPCs (4 requests of 8
+    // beams of 128000 logits: 24.7 us with 16, 28 with 8; 16 x 5 of 50001: 47
+    // with 16, 28 with 8) and lists of one entry per lane, whose joining weighs
+    // less (2 x 64 of 50001, 64 wanted: 254 us with 16, 217 with 8).
     const int vec = bc.type == SSQ_T_F32 ? 4 : 8;
     const long long vectors = (long long)bc.beams * bc.vocab / vec;
     int cs = 1;
-    while (cs < (bc.batch <= 4 ? 16 : 8) && (long long)bc.batch * cs * 2 <= 2 * kSMs
+    while (cs < (bc.batch <= 4 && bc.nsel <= 32 ? 16 : 8) && (long long)bc.batch * cs * 2 <= 2 * kSMs
            && vectors >= (long long)cs * 2 * kBThreads)
         cs *= 2;
     const bool two = bc.nsel > 32;

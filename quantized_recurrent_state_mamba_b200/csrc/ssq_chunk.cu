@@ -781,6 +781,7 @@ chunk_kernel(const __grid_constant__ PoolView pv, const __grid_constant__ Ragged
     const int halves = pv.N > 64 ? 2 : 1;           // 64-column halves of C and B
     if (tid == 0) tl.dead = 0;
     if (warp == kElemWarps + 1) tc::alloc(&tl.tmem, kTmemCols);
+    wait_for_last();
     const long long items = (long long)__ldcg(&rc.plan->count) * pairs;
 
     // ---- one item after another: a pair of units of one segment of one run,
@@ -1012,6 +1013,7 @@ segment_join(const __grid_constant__ PoolView pv, const __grid_constant__ Ragged
     constexpr int kRows = kJoinThreads / LPR;        // kRows*N = 128*E floats
     constexpr int kVec = kRows * N / 4 / kJoinThreads;
     __shared__ __align__(16) float stage[kRows * N];
+    let_next_start();
     const int tiles = (pv.P + kRows - 1) / kRows;
     const int per = tiles * pv.H;
     const int b = blockIdx.x / per, unit = blockIdx.x - b * per;
@@ -1146,8 +1148,18 @@ cudaError_t launch_pass(const PoolView& pv, const RaggedCall& rc, const ChunkMap
     const long long items = chunk_items(pv.H, pv.P, pv.G, rc.units_per_block) * rc.batch * rc.nseg;
     if (items > 0x3fffffffLL) return cudaErrorInvalidConfiguration;
     const unsigned blocks = (unsigned)(items < kSMs ? items : kSMs);
-    chunk_kernel<STATE><<<blocks, kCThreadsTotal, kSmemBytes, st>>>(pv, rc, maps, fmt);
-    return cudaGetLastError();
+    cudaLaunchConfig_t cfg;
+    std::memset(&cfg, 0, sizeof(cfg));
+    cfg.gridDim = dim3(blocks);
+    cfg.blockDim = dim3(kCThreadsTotal);
+    cfg.dynamicSmemBytes = kSmemBytes;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, chunk_kernel<STATE>, pv, rc, maps, fmt);
 }
 
 }  // namespace

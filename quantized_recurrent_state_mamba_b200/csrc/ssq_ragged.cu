@@ -319,6 +319,7 @@ tokens_kernel(const __grid_constant__ PoolView pv, const __grid_constant__ Ragge
     __shared__ float sLam[kTok], sDt[kTok];
     __shared__ int list[kThreads], count[kThreads / 32];
 
+    let_next_start();
     if (rc.plan && blockIdx.x == 0) write_plan(pv, rc);
     static_assert(kTok >= kThreads / 32, "a staged row for every warp");
     if (!state_pass)

@@ -62,6 +62,18 @@ __device__ __forceinline__ Run ragged_run(const PoolView& pv, const RaggedCall& 
     return r;
 }
 
+// The chunk kernel's blocks may start while the kernel before it in the call
+// runs (they set themselves up meanwhile) and wait for its end before they read
+// anything; the kernel before lets them start with its first instruction.
+__device__ __forceinline__ void let_next_start()
+{
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+__device__ __forceinline__ void wait_for_last()
+{
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
 // Segments of a run.
 __device__ __forceinline__ int run_segments(const RaggedCall& rc, int len)
 {
