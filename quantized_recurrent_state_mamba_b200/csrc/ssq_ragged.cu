@@ -159,37 +159,73 @@ __device__ __forceinline__ void single_tokens(const PoolView& pv, const RaggedCa
     }
 }
 
-// The chunk kernel's work list, in the order of the requests: one block.
+// The chunk kernel's work list, by one block: the longest runs first, in eighths
+// of max_len and within one in the order of the requests.  (In the order of the
+// requests alone a long run that comes late keeps a few blocks busy at the end:
+// runs of 4096, 777, 2049, 130 and 3001 tokens of 128 heads take 255 us that
+// way, 213 us this way.)
+constexpr int kLevels = 8;
 __device__ __forceinline__ void write_plan(const PoolView& pv, const RaggedCall& rc)
 {
-    __shared__ int warp_sum[kThreads / 32];
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid / 32, warps = kThreads / 32;
-    int base = 0;
-    for (int b0 = 0; b0 < rc.batch; b0 += kThreads) {
-        const int b = b0 + tid;
-        int n = 0;
-        if (b < rc.batch) {
-            const Run run = ragged_run(pv, rc, b, false);
-            if (run.ok && run.len >= rc.chunk_min) n = run_segments(rc, run.len);
-        }
-        int upto = n;                                // of this warp's requests
+    constexpr int warps = kThreads / 32;
+    __shared__ int total[kLevels], warp_sum[kLevels][warps];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid / 32;
+    // entries of a request, and its level
+    auto entries = [&](int b, int* level) {
+        *level = 0;
+        if (b >= rc.batch) return 0;
+        const Run run = ragged_run(pv, rc, b, false);
+        if (!run.ok || run.len < rc.chunk_min) return 0;
+        *level = kLevels - 1 - (int)(((long long)run.len * kLevels - 1) / rc.max_len);
+        return run_segments(rc, run.len);
+    };
+    if (tid < kLevels) total[tid] = 0;
+    __syncthreads();
+    int level0, level;
+    const int n0 = entries(tid, &level0);            // most batches end here
+    if (n0) atomicAdd(&total[level0], n0);
+    for (int b = tid + kThreads; b < rc.batch; b += kThreads) {
+        const int n = entries(b, &level);
+        if (n) atomicAdd(&total[level], n);
+    }
+    __syncthreads();
+    int base[kLevels], count = 0;                    // where a level's next entry goes
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int v = __shfl_up_sync(0xffffffffu, upto, o);
-            if (lane >= o) upto += v;
+    for (int l = 0; l < kLevels; ++l) {
+        base[l] = count;
+        count += total[l];
+    }
+    for (int b0 = 0; b0 < rc.batch; b0 += kThreads) {
+        int n = n0;
+        level = level0;
+        if (b0 > 0) n = entries(b0 + tid, &level);
+        int at = 0;                                  // among its warp's of its level
+#pragma unroll
+        for (int l = 0; l < kLevels; ++l) {
+            const int mine = l == level ? n : 0;
+            int upto = mine;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int v = __shfl_up_sync(0xffffffffu, upto, o);
+                if (lane >= o) upto += v;
+            }
+            if (l == level) at = upto - mine;
+            if (lane == 31) warp_sum[l][warp] = upto;
         }
-        if (lane == 31) warp_sum[warp] = upto;
         __syncthreads();
-        int at = base + upto - n;
-        for (int w = 0; w < warps; ++w) {
-            if (w < warp) at += warp_sum[w];
-            base += warp_sum[w];
+#pragma unroll
+        for (int l = 0; l < kLevels; ++l) {
+            if (l == level) at += base[l];
+            for (int w = 0; w < warps; ++w) {
+                if (l == level && w < warp) at += warp_sum[l][w];
+                base[l] += warp_sum[l][w];
+            }
         }
-        for (int k = 0; k < n; ++k) rc.plan->entry[at + k] = make_int2(b, k);
+        for (int k = 0; k < n; ++k) rc.plan->entry[at + k] = make_int2(b0 + tid, k);
         __syncthreads();
     }
     if (tid == 0) {
-        rc.plan->count = base;
+        rc.plan->count = count;
         rc.plan->next[0] = 0;
         rc.plan->next[1] = 0;
     }
