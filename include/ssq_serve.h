@@ -94,7 +94,8 @@ SSQ_API ssq_status ssq_prefill_ragged_workspace(const ssq_config* cfg, int batch
  * its own request only; in a chunk a non-finite x_p makes y and the state of
  * its row p NaN.
  *
- *   slot_idx   device int32 [batch] or NULL (slot b)
+ *   slot_idx   device int32 [batch] or NULL (slot b); the slots of one call
+ *              are distinct
  *   cu_tokens  device int32 [batch+1], not decreasing, within [0, total]; a
  *              request whose range is not valid or is longer than max_len is
  *              skipped (SSQ_DEVERR_TOKENS)

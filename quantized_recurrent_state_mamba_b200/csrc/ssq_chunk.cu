@@ -31,6 +31,18 @@
 // (in which 0 * NaN would reach earlier tokens) and makes y_ip, i >= j, and
 // the state's row p NaN.
 //
+// What bounds it: per unit and chunk the products read 192 KB of shared memory
+// and the element work and copies move 160 KB (a probe of such reads and writes
+// runs at 92 bytes a clock), and inside a chunk scores, weights, product and
+// state follow one another.  One unit alone takes 6000 cycles a chunk, two
+// 7700; 8 runs of 2048 tokens of 32 heads x 64 x 128, int8: 82 us, tensor pipe
+// 23 %, issue 34 %.  Tried: 128 threads a unit instead of 256 (143 to 111 us
+// with a warp per sequence of products), `lane == 0` instead of elect.sync
+// (111 to 99), barrier tests with a time hint (they poll), states and y in TMEM
+// with front and back warps on different chunks (118), setmaxnreg (spills).
+// Registers are kept below what spills: beside 221 KB of shared memory the L1
+// is small, and a reload takes about 500 cycles.
+//
 // Long runs on few heads are cut into segments: a first pass computes each
 // segment's own state and decay, segment_join turns them into the states
 // the segments start from, and the main pass runs all segments at once.

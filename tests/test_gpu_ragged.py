@@ -564,3 +564,16 @@ def test_many_requests():
     y, b, a, pool, cfg = run(ssq, i, lens, "f32", fresh=fresh)
     check(i, lens, "f32", y, b, a, fresh=fresh)
     assert ssq.ssq_pool_error(cfg, pool) == 0
+
+
+def test_many_runs_in_chunks():
+    """Runs of every length up to max_len, more than blocks and threads, in an
+    order that is not theirs by length."""
+    ssq = require_gpu()
+    lens = [40, 1, 256, 100] + [0] * 250 + [200, 33, 129, 64, 1, 256, 180, 90, 31]
+    i = inputs(lens, 64, 8, 16, 1, torch.bfloat16, 20)
+    y, b, a, pool, cfg = run(ssq, i, lens, "i8s")
+    check(i, lens, "i8s", y, b, a)
+    again, _, a2, _, _ = run(ssq, i, lens, "i8s")
+    assert torch.equal(y, again) and torch.equal(a, a2)
+    assert ssq.ssq_pool_error(cfg, pool) == 0
