@@ -86,12 +86,13 @@ constexpr int kOffTail = Mem<false>::s + 2 * kTileX;
 static_assert(Mem<true>::xs + 6 * kTileX <= kOffTail, "the passes share one size");
 constexpr int kMaxRing = 4;
 
-struct UnitArrays {
+struct alignas(16) UnitArrays {
     float f[kL];        // dt_j exp(q_j)
     float nr[kL];       // log2(dt_j) - r_j
-    float block[4];     // sums of the four blocks
+    // of a chunk and the next, by the chunk's parity
+    float block[2][4];  // sums of the four blocks
+    int any_bad[2];
     int bad[kPT];       // first token of the chunk with a non-finite x in row p
-    int any_bad;
     float decay;        // of the segment so far (first pass)
     float A2, D;        // A log2(e) and D of the unit's head
 };
@@ -383,7 +384,7 @@ __device__ __forceinline__ bool unit_loop(const PoolView& pv, const RaggedCall& 
         write_state();
     }
     if (hf == 0 && t < kPT) ua.bad[t] = kL;
-    if (hf == 0 && t == 0) ua.any_bad = 0;
+    if (hf == 0 && t < 2) ua.any_bad[t] = 0;
     const bool leader = hf == 0 && t == 0;          // issues the unit's stores
 
     const int tok0 = wk.run.t0 + wk.c0 * kL;        // the segment's first token
@@ -394,21 +395,22 @@ __device__ __forceinline__ bool unit_loop(const PoolView& pv, const RaggedCall& 
     };
     float dt = dt_of(0);
 
-    for (int c = 0; c < wk.nc; ++c) {
-        const int Lc = min(kL, left0 - c * kL);
-        // ---- running sums: forward, and by one half backward ----
+    // A chunk's running sums, forward and by one half backward, are taken while
+    // the tensor cores have the last product of the chunk before, and written
+    // once that product is done: every thread has read the old ones by then.
+    float r, mine;
+    auto sums = [&](int c) {
         float a = __fmul_rn(dt, ua.A2);
         if (a < kStepFloor) a = kStepFloor;         // a NaN stays
-        if (t >= Lc) a = 0.0f;                      // dt is 0 there, A may be infinite
-        float r = a;
+        if (t >= left0 - c * kL) a = 0.0f;          // dt is 0 there, A may be infinite
+        r = a;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const float v = __shfl_up_sync(0xffffffffu, r, o);
             if (lane >= o) r += v;
         }
         if (hf == 0) {
-            ua.nr[t] = __fsub_rn(lg2(dt), r);
-            if (lane == 31) ua.block[w] = r;
+            mine = __fsub_rn(lg2(dt), r);
         } else {
             float q = __shfl_down_sync(0xffffffffu, a, 1);
             if (lane == 31) q = 0.0f;
@@ -417,13 +419,23 @@ __device__ __forceinline__ bool unit_loop(const PoolView& pv, const RaggedCall& 
                 const float v = __shfl_down_sync(0xffffffffu, q, o);
                 if (lane + o < 32) q += v;
             }
-            ua.f[t] = __fmul_rn(dt, ex2(q));
+            mine = __fmul_rn(dt, ex2(q));
         }
         dt = dt_of(c + 1);
-        unit_sync(u);
+    };
+    auto write_sums = [&](int c) {                  // a unit_sync before their use
+        (hf == 0 ? ua.nr : ua.f)[t] = mine;
+        if (hf == 0 && lane == 31) ua.block[c & 1][w] = r;
+    };
+    sums(0);
+    write_sums(0);
+    unit_sync(u);
+
+    for (int c = 0; c < wk.nc; ++c) {
+        const int Lc = min(kL, left0 - c * kL);
         // the sums of the chunk's blocks, read again where they are needed
         // (registers are short here)
-        const float4& bs = *reinterpret_cast<const float4*>(ua.block);
+        const float4& bs = *reinterpret_cast<const float4*>(ua.block[c & 1]);
         float wj;
         {
             float behind = 0.0f;
@@ -451,7 +463,7 @@ __device__ __forceinline__ bool unit_loop(const PoolView& pv, const RaggedCall& 
                                       : weigh_x3<true, !STATE>(xrow, xs, at0, wj, true);
         if (bad) {
             // rare: take the non-finite entries of this token out
-            ua.any_bad = 1;
+            ua.any_bad[c & 1] = 1;
             for (int p = kPH * hf; p < kPH * hf + kPH; ++p) {
                 const unsigned pa = swz(t, p >> 3) + (p & 7) * 2;
                 unsigned short v;
@@ -533,8 +545,13 @@ __device__ __forceinline__ bool unit_loop(const PoolView& pv, const RaggedCall& 
         }
 
         // ---- state ----
+        if (STATE && c + 1 < wk.nc) sums(c + 1);
         wait(&tl.ds_full[u], c & 1);
         tc::fence_after();
+        if constexpr (STATE) {
+            if (leader) mbar_arrive(&tl.x_empty[xslot]);    // (read by all)
+            if (c + 1 < wk.nc) write_sums(c + 1);
+        }
         {
             const float lam = ex2((bs.x + bs.y) + (bs.z + bs.w));
             if (STATE && leader) ua.decay = __fmul_rn(ua.decay, lam);
@@ -558,13 +575,12 @@ __device__ __forceinline__ bool unit_loop(const PoolView& pv, const RaggedCall& 
             }
         }
         if constexpr (STATE) {
-            unit_sync(u);                           // the x buffer has been read by all
-            if (leader) mbar_arrive(&tl.x_empty[xslot]);
-            if (ua.any_bad) {
+            unit_sync(u);
+            if (ua.any_bad[c & 1]) {
                 bad_state(ua, hf, S);
                 unit_sync(u);
                 if (hf == 0 && t < kPT) ua.bad[t] = kL;
-                if (leader) ua.any_bad = 0;
+                if (leader) ua.any_bad[c & 1] = 0;
                 unit_sync(u);
             }
         } else {
@@ -573,8 +589,10 @@ __device__ __forceinline__ bool unit_loop(const PoolView& pv, const RaggedCall& 
                                  + (w > 2 ? bs.z : 0.0f);
             const float ei = ex2(r + before);
             const float2 e2 = make_float2(ei, ei), D2 = make_float2(ua.D, ua.D);
+            if (c + 1 < wk.nc) sums(c + 1);
             wait(&tl.y_full[u], c & 1);
             tc::fence_after();
+            if (c + 1 < wk.nc) write_sums(c + 1);
             if (c + 1 < wk.nc) write_state();       // Y2 of this chunk has read the old one
 #pragma unroll
             for (int k = 0; k < kPH; k += 8) {
@@ -599,7 +617,7 @@ __device__ __forceinline__ bool unit_loop(const PoolView& pv, const RaggedCall& 
             tc::fence_before();
             fence_proxy_async();
             unit_sync(u);
-            if (ua.any_bad) {
+            if (ua.any_bad[c & 1]) {
                 // rare: NaN for the rows with a non-finite x, from its token on
                 bad_state(ua, hf, S);
                 if (c + 1 < wk.nc) write_state();
@@ -612,7 +630,7 @@ __device__ __forceinline__ bool unit_loop(const PoolView& pv, const RaggedCall& 
                 fence_proxy_async();
                 unit_sync(u);
                 if (hf == 0 && t < kPT) ua.bad[t] = kL;
-                if (leader) ua.any_bad = 0;
+                if (leader) ua.any_bad[c & 1] = 0;
                 unit_sync(u);
             }
             const int tok = tok0 + c * kL, p0 = wk.p0[u], h = wk.h[u];
