@@ -71,24 +71,44 @@ constexpr float kStepFloor = -1500.0f;
 // Shared memory, from its 1024-byte aligned start (the swizzle's period).
 constexpr int kTileCB = kL * 256;       // C or B: two halves of [128][64] bf16
 constexpr int kTileX = kL * 128;        // [128][64] bf16
-// Places of the rings: C and B take turns in three; the first pass over
-// segments loads no C and keeps no state operand, so it has a ring of two for
-// B, one more place for x, and a buffer of w X for each unit.
-template <bool STATE>
+// The passes: kMain; kStates, the first pass over segments; kStates2, the same
+// where every stored row takes two parts of w X, which leaves room for two
+// buffers of them, so that a chunk's elements overlap the product before (one
+// run of 65536 tokens of 24 heads, int8: 305 us a call with one buffer, 286 with
+// two).
+constexpr int kMain = 0, kStates = 1, kStates2 = 2;
+// Places of the rings: C and B take turns in three; the first pass loads no C
+// and keeps no state operand, so it has a ring of two for B and buffers of w X
+// for each unit.
+template <int PASS>
 struct Mem {
-    static constexpr int ring_cb = STATE ? 2 : 3, ring_x = STATE ? 4 : 3;
+    static constexpr int ring_cb = PASS ? 2 : 3;
+    static constexpr int ring_x = PASS == kStates2 ? 2 : PASS == kStates ? 4 : 3;
     static constexpr int x = ring_cb * kTileCB;
     static constexpr int xs = x + ring_x * kTileX;   // up to three bf16 parts of w X
-    static constexpr int xs_unit = STATE ? 3 * kTileX : 0;
+    static constexpr int xs_unit = PASS == kStates2 ? 2 * kTileX : PASS == kStates ? 3 * kTileX : 0;
+    static constexpr int xs_next = PASS == kStates2 ? 2 * xs_unit : 0;   // of the next chunk
     static constexpr int s = xs + 3 * kTileX;        // states in bf16, one per unit
 };
-constexpr int kOffTail = Mem<false>::s + 2 * kTileX;
-static_assert(Mem<true>::xs + 6 * kTileX <= kOffTail, "the passes share one size");
+constexpr int kOffTail = Mem<kMain>::s + 2 * kTileX;
+static_assert(Mem<kStates>::xs + 6 * kTileX <= kOffTail &&
+              Mem<kStates2>::xs + 8 * kTileX <= kOffTail, "the passes share one size");
 constexpr int kMaxRing = 4;
+
+// Barriers of unit u and chunk c whose place and phase go by the chunk: one per
+// unit; with two chunks under way two, since a second phase may end before the
+// first is waited for.
+template <int PASS>
+__device__ __forceinline__ int place_of(int u, int c) { return PASS == kStates2 ? u + 2 * (c & 1) : u; }
+template <int PASS>
+__device__ __forceinline__ unsigned phase_of(int c)
+{
+    return (unsigned)(PASS == kStates2 ? c >> 1 : c) & 1u;
+}
 
 struct alignas(16) UnitArrays {
     float f[kL];        // dt_j exp(q_j)
-    float nr[kL];       // log2(dt_j) - r_j
+    float nr[kL];       // log2(dt_j) - r_j; with kStates2 f of odd chunks
     // of a chunk and the next, by the chunk's parity
     float block[2][4];  // sums of the four blocks
     int any_bad[2];
@@ -107,7 +127,7 @@ struct Work {
 struct Tail {
     UnitArrays unit[2];
     uint64_t cb_full[kMaxRing], cb_empty[kMaxRing], x_full[kMaxRing], x_empty[kMaxRing];
-    uint64_t xs_ready[2], ds_full[2], m_ready[2], y_full[2], g_full, g_free, b_ready, drained[3];
+    uint64_t xs_ready[4], ds_full[4], m_ready[2], y_full[2], g_full, g_free, b_ready, drained[3];
     uint32_t tmem;
     Work work;
     int parts;          // of w X in a whole chunk
@@ -123,9 +143,13 @@ constexpr uint32_t kColG = 0;
 __host__ __device__ constexpr uint32_t col_m(int u) { return 128 + 192 * u; }
 __host__ __device__ constexpr uint32_t col_y1(int u) { return col_m(u) + 64; }
 __host__ __device__ constexpr uint32_t col_y2(int u) { return col_m(u) + 128; }
-// dS takes Y1's columns; in the first pass the units' lie side by side.
-template <bool STATE>
-__host__ __device__ constexpr uint32_t col_ds(int u) { return STATE ? 128 + 64 * u : col_y1(u); }
+// dS takes Y1's columns; in the first pass the units' lie side by side, with two
+// buffers behind one another.
+template <int PASS>
+__host__ __device__ constexpr uint32_t col_ds(int u, int c)
+{
+    return PASS ? 128 + 64 * u + (PASS == kStates2 ? 128 * (c & 1) : 0) : col_y1(u);
+}
 
 __device__ __forceinline__ void unit_sync(int u)
 {
@@ -348,19 +372,20 @@ __device__ __forceinline__ void bad_state(const UnitArrays& ua, int hf, float (&
         if (ua.bad[kPH * hf + p] < kL) S[p] = __int_as_float(0x7fffffff);
 }
 
-template <bool STATE>
+template <int PASS>
 __device__ __forceinline__ bool unit_loop(const PoolView& pv, const RaggedCall& rc,
                                           const CUtensorMap* ymap, const Work& wk,
-                                          unsigned char* sm, unsigned base, Tail& tl, uint32_t tmem, int u, int t,
-                                          int hf, float (&S)[kPH])
+                                          unsigned char* sm, unsigned base, Tail& tl,
+                                          uint32_t tmem, int u, int t, int hf, float (&S)[kPH])
 {
+    constexpr bool STATE = PASS != kMain, AHEAD = PASS == kStates2;
     const int lane = t & 31, w = t >> 5;
     const int nu = wk.nu;
     UnitArrays& ua = tl.unit[u];
     const uint32_t tm = tmem + ((uint32_t)(w * 32) << 16);
-    using M = Mem<STATE>;
+    using M = Mem<PASS>;
     const unsigned s_op = base + M::s + u * kTileX;
-    const unsigned xs = base + M::xs + u * M::xs_unit;
+    const unsigned xs0 = base + M::xs + u * M::xs_unit;
     const unsigned at0 = swz(t, 4 * hf);            // piece i of the thread's half line: at0 ^ 16 i
     bool ok = true;
     auto wait = [&](uint64_t* bar, unsigned parity) {
@@ -424,12 +449,38 @@ __device__ __forceinline__ bool unit_loop(const PoolView& pv, const RaggedCall& 
         dt = dt_of(c + 1);
     };
     auto write_sums = [&](int c) {                  // a unit_sync before their use
-        (hf == 0 ? ua.nr : ua.f)[t] = mine;
+        if constexpr (AHEAD) {
+            if (hf == 1) (c & 1 ? ua.nr : ua.f)[t] = mine;
+        } else {
+            (hf == 0 ? ua.nr : ua.f)[t] = mine;
+        }
         if (hf == 0 && lane == 31) ua.block[c & 1][w] = r;
     };
     sums(0);
     write_sums(0);
     unit_sync(u);
+
+    auto add_state = [&](int c, float lam) {        // S = lam S + dS of chunk c
+        const float2 l2 = make_float2(lam, lam);
+#pragma unroll
+        for (int k = 0; k < kPH; k += 16) {
+            float d[16];
+            tc::ld16(tm + col_ds<PASS>(u, c) + kPH * hf + k, d);
+            tc::wait_ld(d);
+            if (k + 16 == kPH) {
+                tc::fence_before();
+                if constexpr (!STATE) mbar_arrive(&tl.m_ready[u]);
+            }
+#pragma unroll
+            for (int m = 0; m < 16; m += 2) {
+                const float2 v = fma2(l2, make_float2(S[k + m], S[k + m + 1]),
+                                      make_float2(d[m], d[m + 1]));
+                S[k + m] = v.x;
+                S[k + m + 1] = v.y;
+            }
+        }
+    };
+    float lam_before = 0.0f;                        // kStates2: of the chunk before
 
     for (int c = 0; c < wk.nc; ++c) {
         const int Lc = min(kL, left0 - c * kL);
@@ -442,15 +493,16 @@ __device__ __forceinline__ bool unit_loop(const PoolView& pv, const RaggedCall& 
             if (w < 3) behind = bs.w;
             if (w < 2) behind += bs.z;
             if (w < 1) behind += bs.y;
-            wj = __fmul_rn(ua.f[t], ex2(behind));
+            wj = __fmul_rn((AHEAD && (c & 1) ? ua.nr : ua.f)[t], ex2(behind));
         }
 
         // ---- w X in parts ----
         const int kx = c * nu + u, xslot = kx % M::ring_x;
         const unsigned xrow = base + M::x + xslot * kTileX;
         wait(&tl.x_full[xslot], (kx / M::ring_x) & 1);
+        const unsigned xs = xs0 + (c & 1) * M::xs_next;
         if constexpr (STATE) {
-            if (c > 0) wait(&tl.ds_full[u], (c - 1) & 1);       // (seen before: at once)
+            // (the product that read w X's buffer last has been waited for)
         } else if (nu > 1) {
             // the other unit's product has read the shared buffer
             if (u == 1)
@@ -458,7 +510,8 @@ __device__ __forceinline__ bool unit_loop(const PoolView& pv, const RaggedCall& 
             else if (c > 0)
                 wait(&tl.ds_full[1], (c - 1) & 1);
         }
-        const bool bad = Lc < kL ? weigh_x3<false, !STATE>(xrow, xs, at0, wj, t < Lc)
+        const bool bad = AHEAD ? weigh_x2(xrow, xs, at0, wj)      // whole chunks only
+                         : Lc < kL ? weigh_x3<false, !STATE>(xrow, xs, at0, wj, t < Lc)
                          : tl.parts == 2 ? weigh_x2(xrow, xs, at0, wj)
                                       : weigh_x3<true, !STATE>(xrow, xs, at0, wj, true);
         if (bad) {
@@ -480,7 +533,7 @@ __device__ __forceinline__ bool unit_loop(const PoolView& pv, const RaggedCall& 
         }
         __syncwarp();
         fence_proxy_async();
-        mbar_arrive(&tl.xs_ready[u]);
+        mbar_arrive(&tl.xs_ready[place_of<PASS>(u, c)]);
         if (!STATE && leader && c > 0) {
             // y of the chunk before has been read from its x buffer
             bulk_wait_read<0>();
@@ -545,38 +598,35 @@ __device__ __forceinline__ bool unit_loop(const PoolView& pv, const RaggedCall& 
         }
 
         // ---- state ----
-        if (STATE && c + 1 < wk.nc) sums(c + 1);
-        wait(&tl.ds_full[u], c & 1);
-        tc::fence_after();
-        if constexpr (STATE) {
-            if (leader) mbar_arrive(&tl.x_empty[xslot]);    // (read by all)
-            if (c + 1 < wk.nc) write_sums(c + 1);
-        }
-        {
-            const float lam = ex2((bs.x + bs.y) + (bs.z + bs.w));
-            if (STATE && leader) ua.decay = __fmul_rn(ua.decay, lam);
-            const float2 l2 = make_float2(lam, lam);
-#pragma unroll
-            for (int k = 0; k < kPH; k += 16) {
-                float d[16];
-                tc::ld16(tm + col_ds<STATE>(u) + kPH * hf + k, d);
-                tc::wait_ld(d);
-                if (k + 16 == kPH) {
-                    tc::fence_before();
-                    if constexpr (!STATE) mbar_arrive(&tl.m_ready[u]);
-                }
-#pragma unroll
-                for (int m = 0; m < 16; m += 2) {
-                    const float2 v = fma2(l2, make_float2(S[k + m], S[k + m + 1]),
-                                          make_float2(d[m], d[m + 1]));
-                    S[k + m] = v.x;
-                    S[k + m + 1] = v.y;
-                }
+        const float lam = ex2((bs.x + bs.y) + (bs.z + bs.w));
+        if (STATE && leader) ua.decay = __fmul_rn(ua.decay, lam);
+        if constexpr (AHEAD) {
+            // this chunk's product runs meanwhile: the sums of the next one, and
+            // the state of the one before
+            if (c + 1 < wk.nc) {
+                sums(c + 1);
+                write_sums(c + 1);
             }
+            if (c > 0) {
+                wait(&tl.ds_full[place_of<PASS>(u, c - 1)], phase_of<PASS>(c - 1));
+                tc::fence_after();
+                add_state(c - 1, lam_before);
+            }
+            lam_before = lam;
+        } else {
+            if (STATE && c + 1 < wk.nc) sums(c + 1);
+            wait(&tl.ds_full[u], c & 1);
+            tc::fence_after();
+            if constexpr (STATE) {
+                if (leader) mbar_arrive(&tl.x_empty[xslot]);    // (read by all)
+                if (c + 1 < wk.nc) write_sums(c + 1);
+            }
+            add_state(c, lam);
         }
         if constexpr (STATE) {
             unit_sync(u);
-            if (ua.any_bad[c & 1]) {
+            if (AHEAD && leader) mbar_arrive(&tl.x_empty[xslot]);   // (read by all)
+            if (ua.any_bad[c & 1]) {                // (NaN stays through what is added)
                 bad_state(ua, hf, S);
                 unit_sync(u);
                 if (hf == 0 && t < kPT) ua.bad[t] = kL;
@@ -651,6 +701,11 @@ __device__ __forceinline__ bool unit_loop(const PoolView& pv, const RaggedCall& 
             }
         }
     }
+    if constexpr (AHEAD) {
+        wait(&tl.ds_full[place_of<PASS>(u, wk.nc - 1)], phase_of<PASS>(wk.nc - 1));
+        tc::fence_after();
+        add_state(wk.nc - 1, lam_before);
+    }
     if (!STATE && leader) bulk_wait_read<0>();      // the buffers outlive the stores
     __syncwarp();
     return ok;
@@ -660,15 +715,15 @@ __device__ __forceinline__ bool unit_loop(const PoolView& pv, const RaggedCall& 
 // The products, one warp per sequence of them; lane 0 issues.  Every operand
 // address is a function of the chunk counter alone.
 // ---------------------------------------------------------------------------
-template <bool STATE>
-__device__ __forceinline__ int slot_b(int c) { return (STATE ? c : 2 * c + 1) % Mem<STATE>::ring_cb; }
-template <bool STATE>
+template <int PASS>
+__device__ __forceinline__ int slot_b(int c) { return (PASS ? c : 2 * c + 1) % Mem<PASS>::ring_cb; }
+template <int PASS>
 __device__ __forceinline__ unsigned phase_b(int c)
 {
-    return (unsigned)((STATE ? c : 2 * c + 1) / Mem<STATE>::ring_cb) & 1u;
+    return (unsigned)((PASS ? c : 2 * c + 1) / Mem<PASS>::ring_cb) & 1u;
 }
-__device__ __forceinline__ int slot_c(int c) { return 2 * c % Mem<false>::ring_cb; }
-__device__ __forceinline__ unsigned phase_c(int c) { return (unsigned)(2 * c / Mem<false>::ring_cb) & 1u; }
+__device__ __forceinline__ int slot_c(int c) { return 2 * c % Mem<kMain>::ring_cb; }
+__device__ __forceinline__ unsigned phase_c(int c) { return (unsigned)(2 * c / Mem<kMain>::ring_cb) & 1u; }
 
 // G = C B^T of every chunk.
 __device__ __forceinline__ bool issue_g(unsigned base, Tail& tl, uint32_t tmem, int nc,
@@ -677,10 +732,10 @@ __device__ __forceinline__ bool issue_g(unsigned base, Tail& tl, uint32_t tmem, 
     constexpr uint32_t kShape = tc::shape(128, 128, false, false);
     for (int c = 0; c < nc; ++c) {
         bool ok = tc::wait_phase(&tl.cb_full[slot_c(c)], phase_c(c));
-        ok = ok && tc::wait_phase(&tl.cb_full[slot_b<false>(c)], phase_b<false>(c));
+        ok = ok && tc::wait_phase(&tl.cb_full[slot_b<kMain>(c)], phase_b<kMain>(c));
         if (ok && c > 0) ok = tc::wait_phase(&tl.g_free, (c - 1) & 1);
         if (!__all_sync(0xffffffffu, ok)) return false;
-        const unsigned sc = base + slot_c(c) * kTileCB, sb = base + slot_b<false>(c) * kTileCB;
+        const unsigned sc = base + slot_c(c) * kTileCB, sb = base + slot_b<kMain>(c) * kTileCB;
         if (c == nc - 1 && last_len < kL) {
             // lines of B past the run's end
             for (int i = lane; i < (kL - last_len) * 8; i += 32)
@@ -701,7 +756,7 @@ __device__ __forceinline__ bool issue_g(unsigned base, Tail& tl, uint32_t tmem, 
                 }
             tc::commit(&tl.g_full);
             tc::commit(&tl.cb_empty[slot_c(c)]);
-            tc::commit(&tl.cb_empty[slot_b<false>(c)]);
+            tc::commit(&tl.cb_empty[slot_b<kMain>(c)]);
         }
         __syncwarp();
     }
@@ -710,29 +765,31 @@ __device__ __forceinline__ bool issue_g(unsigned base, Tail& tl, uint32_t tmem, 
 
 // First pass: dS of both units in one product (B is read once for the two;
 // the units' parts of w X are one operand of two 64-row pieces).
-template <int NU>
+template <int PASS, int NU>
 __device__ __forceinline__ bool issue_state(unsigned base, Tail& tl, uint32_t tmem, int nc,
                                             int parts)
 {
     constexpr uint32_t kShape = tc::shape(128, 64 * NU, true, true);
-    using M = Mem<true>;
+    using M = Mem<PASS>;
     for (int c = 0; c < nc; ++c) {
-        const unsigned sb = base + slot_b<true>(c) * kTileCB;
-        bool ok = tc::wait_phase(&tl.cb_full[slot_b<true>(c)], phase_b<true>(c));
-        for (int u = 0; u < NU; ++u) ok = ok && tc::wait_phase(&tl.xs_ready[u], c & 1);
+        const unsigned sb = base + slot_b<PASS>(c) * kTileCB;
+        bool ok = tc::wait_phase(&tl.cb_full[slot_b<PASS>(c)], phase_b<PASS>(c));
+        for (int u = 0; u < NU; ++u)
+            ok = ok && tc::wait_phase(&tl.xs_ready[place_of<PASS>(u, c)], phase_of<PASS>(c));
         if (!__all_sync(0xffffffffu, ok)) return false;
         if (tc::elect()) {
             tc::fence_after();
-            const uint64_t db = tc::operand(sb, kTileX), dx = tc::operand(base + M::xs, M::xs_unit);
+            const uint64_t db = tc::operand(sb, kTileX);
+            const uint64_t dx = tc::operand(base + M::xs + (c & 1) * M::xs_next, M::xs_unit);
 #pragma unroll
             for (int part = 0; part < 3; ++part)
                 if (part < parts)
 #pragma unroll
                     for (int k = 0; k < kL / 16; ++k)
-                        tc::mma(tmem + col_ds<true>(0), db + k * 128,
+                        tc::mma(tmem + col_ds<PASS>(0, c), db + k * 128,
                                 dx + (part * kTileX >> 4) + k * 128, kShape, part + k > 0);
-            for (int u = 0; u < NU; ++u) tc::commit(&tl.ds_full[u]);
-            tc::commit(&tl.cb_empty[slot_b<true>(c)]);
+            for (int u = 0; u < NU; ++u) tc::commit(&tl.ds_full[place_of<PASS>(u, c)]);
+            tc::commit(&tl.cb_empty[slot_b<PASS>(c)]);
         }
         __syncwarp();
     }
@@ -746,10 +803,10 @@ __device__ __forceinline__ bool issue_unit(unsigned base, Tail& tl, uint32_t tme
 {
     constexpr uint32_t kShapeY = tc::shape(128, 64, false, true);
     constexpr uint32_t kShapeS = tc::shape(128, 64, true, true);
-    using M = Mem<false>;
+    using M = Mem<kMain>;
     const unsigned xs = base + M::xs, so = base + M::s + U * kTileX;
     for (int c = 0; c < nc; ++c) {
-        const unsigned sb = base + slot_b<false>(c) * kTileCB;
+        const unsigned sb = base + slot_b<kMain>(c) * kTileCB;
         bool ok = tc::wait_phase(&tl.b_ready, c & 1);
         ok = ok && tc::wait_phase(&tl.xs_ready[U], c & 1);
         if (!__all_sync(0xffffffffu, ok)) return false;
@@ -763,10 +820,10 @@ __device__ __forceinline__ bool issue_unit(unsigned base, Tail& tl, uint32_t tme
                 if (part < 2 || three)
 #pragma unroll
                     for (int k = 0; k < kL / 16; ++k)
-                        tc::mma(tmem + col_ds<false>(U), db + k * 128, dx + (part * kTileX >> 4) + k * 128,
+                        tc::mma(tmem + col_ds<kMain>(U, c), db + k * 128, dx + (part * kTileX >> 4) + k * 128,
                                 kShapeS, part + k > 0);
             tc::commit(&tl.ds_full[U]);
-            tc::commit(&tl.cb_empty[slot_b<false>(c)]);
+            tc::commit(&tl.cb_empty[slot_b<kMain>(c)]);
             const uint64_t dc = tc::operand(base + slot_c(c) * kTileCB), ds = tc::operand(so);
 #pragma unroll
             for (int k = 0; k < 8; ++k)
@@ -793,12 +850,13 @@ __device__ __forceinline__ bool issue_unit(unsigned base, Tail& tl, uint32_t tme
     return true;
 }
 
-template <bool STATE>
+template <int PASS>
 __global__ void __launch_bounds__(kCThreadsTotal, 1)
 chunk_kernel(const __grid_constant__ PoolView pv, const __grid_constant__ RaggedCall rc,
              const __grid_constant__ ChunkMaps maps, int fmt)
 {
-    using M = Mem<STATE>;
+    constexpr bool STATE = PASS != kMain;
+    using M = Mem<PASS>;
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     unsigned char* sm = smem_raw;
     const unsigned base = saddr(sm);
@@ -871,8 +929,10 @@ chunk_kernel(const __grid_constant__ PoolView pv, const __grid_constant__ Ragged
             mbar_init(&tl.x_empty[i], 1);
         }
         for (int u = 0; u < 2; ++u) {
-            mbar_init(&tl.xs_ready[u], kWg);
-            mbar_init(&tl.ds_full[u], 1);
+            for (int k = u; k < 4; k += 2) {
+                mbar_init(&tl.xs_ready[k], kWg);
+                mbar_init(&tl.ds_full[k], 1);
+            }
             mbar_init(&tl.m_ready[u], kWg);
             mbar_init(&tl.y_full[u], 1);
         }
@@ -925,7 +985,7 @@ chunk_kernel(const __grid_constant__ PoolView pv, const __grid_constant__ Ragged
         }
         units_sync();       // the staging is read before the loops write there
         if (mine)
-            ok = unit_loop<STATE>(pv, rc, &maps.y, wk, sm, base, tl, tmem, u, t, hf, S);
+            ok = unit_loop<PASS>(pv, rc, &maps.y, wk, sm, base, tl, tmem, u, t, hf, S);
         units_sync();       // the loops are done with the staging
         if (mine && ok) {
             if constexpr (STATE) {
@@ -1001,8 +1061,8 @@ chunk_kernel(const __grid_constant__ PoolView pv, const __grid_constant__ Ragged
         const int last_len = wk.run.len - (wk.c0 + nc - 1) * kL;
         if constexpr (STATE) {
             if (warp == kElemWarps + 1)
-                ok = nu > 1 ? issue_state<2>(base, tl, tmem, nc, parts)
-                            : issue_state<1>(base, tl, tmem, nc, parts);
+                ok = nu > 1 ? issue_state<PASS, 2>(base, tl, tmem, nc, parts)
+                            : issue_state<PASS, 1>(base, tl, tmem, nc, parts);
         } else if (warp == kElemWarps + 1) {
             ok = issue_g(base, tl, tmem, nc, last_len, halves, lane);
         } else if (warp == kElemWarps + 2) {
@@ -1168,12 +1228,12 @@ long long chunk_items(int H, int P, int G, int units_per_block)
     return (long long)((per_group + units_per_block - 1) / units_per_block) * G;
 }
 
-template <bool STATE>
+template <int PASS>
 cudaError_t launch_pass(const PoolView& pv, const RaggedCall& rc, const ChunkMaps& maps, int fmt,
                         cudaStream_t st)
 {
     thread_local int done = -1;
-    cudaError_t e = allow_smem(chunk_kernel<STATE>, kSmemBytes, &done);
+    cudaError_t e = allow_smem(chunk_kernel<PASS>, kSmemBytes, &done);
     if (e != cudaSuccess) return e;
     const long long items = chunk_items(pv.H, pv.P, pv.G, rc.units_per_block) * rc.batch * rc.nseg;
     if (items > 0x3fffffffLL) return cudaErrorInvalidConfiguration;
@@ -1189,7 +1249,7 @@ cudaError_t launch_pass(const PoolView& pv, const RaggedCall& rc, const ChunkMap
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, chunk_kernel<STATE>, pv, rc, maps, fmt);
+    return cudaLaunchKernelEx(&cfg, chunk_kernel<PASS>, pv, rc, maps, fmt);
 }
 
 }  // namespace
@@ -1230,10 +1290,12 @@ cudaError_t launch_ragged_chunks(const PoolView& pv, const RaggedCall& rc, int f
     if (e == cudaSuccess) e = make_map(&maps.C, rc.C, pv.N, pv.G, rc.total, rc.Cs);
     if (e == cudaSuccess) e = make_map(&maps.y, rc.y, pv.P, pv.H, rc.total, rc.ys);
     if (e == cudaSuccess && rc.nseg > 1) {
-        e = launch_pass<true>(pv, rc, maps, fmt, st);
+        const bool two_parts = fmt == SSQ_BF16 || (fmt != SSQ_F32 && pv.Hq == pv.H);
+        e = two_parts ? launch_pass<kStates2>(pv, rc, maps, fmt, st)
+                      : launch_pass<kStates>(pv, rc, maps, fmt, st);
         if (e == cudaSuccess) e = join(pv, rc, fmt, st);
     }
-    if (e == cudaSuccess) e = launch_pass<false>(pv, rc, maps, fmt, st);
+    if (e == cudaSuccess) e = launch_pass<kMain>(pv, rc, maps, fmt, st);
     return e;
 }
 

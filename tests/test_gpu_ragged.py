@@ -226,6 +226,39 @@ def test_chunks_segments(fmt, fresh):
     assert ssq.ssq_pool_error(cfg, pool) == 0
 
 
+@pytest.mark.parametrize("fmt,H,P,N,mask", [("bf16", 3, 64, 128, None), ("i8s", 1, 64, 64, None),
+                                            ("i4a", 3, 40, 128, [1, 0, 1]),
+                                            ("i8a", 2, 72, 16, None)])
+def test_chunks_segments_shapes(fmt, H, P, N, mask):
+    """Segments with an odd number of units, rows that do not fill one, masked
+    heads, and runs that end in every segment."""
+    ssq = require_gpu()
+    lens = [2100, 600, 1030, 0]
+    i = inputs(lens, H, P, N, 1, torch.bfloat16, 21)
+    fresh = torch.tensor([0, 1, 0, 0], dtype=torch.uint8, device="cuda")
+    y, b, a, pool, cfg = run(ssq, i, lens, fmt, fresh=fresh, mask=mask)
+    check(i, lens, fmt, y, b, a, fresh=fresh, mask=mask)
+    assert ssq.ssq_pool_error(cfg, pool) == 0
+
+
+@pytest.mark.parametrize("fmt", ["f32", "bf16"])
+@pytest.mark.parametrize("at", [5, 700, 1990])
+def test_non_finite_in_segments(fmt, at):
+    """A NaN in one row of x makes y and the state of that row NaN from there
+    on, over the segments behind, and nothing else."""
+    ssq = require_gpu()
+    i = inputs([2000], 2, 64, 128, 1, torch.bfloat16, 22)
+    y0, _, a0, _, _ = run(ssq, i, [2000], fmt)
+    i["x"][at, 1, 7] = math.nan
+    y, _, a, _, _ = run(ssq, i, [2000], fmt)
+    hit = torch.zeros_like(y0, dtype=torch.bool)
+    hit[at:, 1, 7] = True
+    assert torch.equal(y[~hit], y0[~hit]) and y[hit].isnan().all()
+    assert a[0, 1, 7].isnan().all()
+    a[0, 1, 7] = a0[0, 1, 7]
+    assert torch.equal(a, a0)
+
+
 @pytest.mark.parametrize("fmt,dtype,N,mask", [("f32", torch.float16, 128, None),
                                               ("bf16", torch.float32, 256, None),
                                               ("i8a", torch.float16, 16, None),
