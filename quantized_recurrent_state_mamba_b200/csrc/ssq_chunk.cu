@@ -36,7 +36,7 @@
 // runs at 92 bytes a clock), and inside a chunk scores, weights, product and
 // state follow one another.  One unit alone takes 6000 cycles a chunk, two
 // 7700; 8 runs of 2048 tokens of 32 heads x 64 x 128, int8: 82 us, tensor pipe
-// 23 %, issue 34 %.  Tried: 128 threads a unit instead of 256 (143 to 111 us
+// 24 %, issue 37 %.  Tried: 128 threads a unit instead of 256 (143 to 111 us
 // with a warp per sequence of products), `lane == 0` instead of elect.sync
 // (111 to 99), barrier tests with a time hint (they poll), states and y in TMEM
 // with front and back warps on different chunks (118), setmaxnreg (spills).
